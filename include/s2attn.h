@@ -62,7 +62,8 @@ typedef enum {
   S2ATTN_ERR_CUDA = 4,           /* a CUDA runtime/driver call or a launch failed */
   S2ATTN_ERR_DEVICE_TIMEOUT = 5, /* a kernel's bounded wait ran out (device status word) */
   S2ATTN_ERR_WORKSPACE = 6,      /* workspace missing or smaller than required */
-  S2ATTN_ERR_DEVICE_BOUNDS = 7   /* debug build only: a kernel's computed index left its tensor (device status word) */
+  S2ATTN_ERR_DEVICE_BOUNDS = 7   /* an index left its tensor (device status word): one computed by a kernel (debug
+                                    build only), or a position, slot or block number in the caller's device data */
 } s2attn_status;
 
 /* Opaque CUDA stream handle (cudaStream_t) without pulling in CUDA headers. */
@@ -303,6 +304,125 @@ S2ATTN_API int s2attn_nf4_qkv(const void* x, const void* codes, const int8_t* sc
 S2ATTN_API int s2attn_nf4_dequant(const void* codes, const int8_t* scale_codes, const float* c2, void* w,
                                   int rows, int K, s2attn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Query/key norm with rotation.  Models with normed heads (Qwen3's layers)
+ * divide every query and key head by its root mean square and weight it
+ * before RoPE:
+ *   r = 1 / sqrt(mean_d x_d^2 + eps),  u_d = r x_d w_d,  y = rotate(u)
+ * with the rotary table of s2attn_rope_table at the row's token.  q, k are
+ * normed by their own weight each (w_q, w_k [D], shared by the heads), fp32
+ * when w_fp32 != 0, else bf16.  Arithmetic is fp32, y is rounded to bf16 once.
+ * B, N, H, Hkv may be any positive sizes (N need not be a tile multiple);
+ * D in {64, 128}; eps > 0 (a normal fp32 number); every pointer 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+
+/* q_out, k_out = rotate(norm(q)), rotate(norm(k)); bf16 [B, N, H, D] and
+ * [B, N, Hkv, D].  q_out may be q and k_out may be k (in place). */
+S2ATTN_API int s2attn_qknorm_rope_fwd(const void* q, const void* k, const void* w_q, const void* w_k,
+                                      const float* table, void* q_out, void* k_out, int B, int N, int H, int Hkv,
+                                      int D, int w_fp32, double eps, s2attn_stream_t stream);
+
+/* Workspace bytes of s2attn_qknorm_rope_bwd (the blocks' partial weight
+ * gradients; 0 for an unsupported head dim). */
+S2ATTN_API size_t s2attn_qknorm_rope_bwd_workspace_bytes(int D);
+
+/*
+ * Backward: from the forward's inputs q, k and the gradients dq_out, dk_out of
+ * its outputs, the gradients dq, dk (bf16) and dw_q, dw_k ([D], the weights'
+ * type; sums over every row, fp32 inside a block and fp64 across blocks, in a
+ * fixed order).  dq may be dq_out and dk may be dk_out (in place).
+ * workspace: 16-byte aligned, s2attn_qknorm_rope_bwd_workspace_bytes(D) bytes,
+ * need not be cleared.  Two launches.
+ */
+S2ATTN_API int s2attn_qknorm_rope_bwd(const void* q, const void* k, const void* w_q, const void* w_k,
+                                      const float* table, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                      void* dw_q, void* dw_k, int B, int N, int H, int Hkv, int D, int w_fp32,
+                                      double eps, void* workspace, size_t workspace_bytes, s2attn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Decoding over a paged cache (dense attention at inference: LongQLoRA post,
+ * section 03, for the few new tokens of many requests).  The cache is
+ *   k_cache, v_cache : bf16 [num_blocks, block_size, Hkv, D]
+ * and request i's key at place p lies in block block_tables[i][p / block_size]
+ * (int32 [R, max_blocks]), row p % block_size; place = block * block_size + row
+ * is a SLOT.  A step of a ragged batch of R requests with T new tokens (request
+ * after request) is: s2attn_cache_plan for the slots, s2attn_cache_append to
+ * put the tokens' keys and values there, s2attn_cache_attn.
+ *
+ * Lengths, tables, positions and slots are device data the host does not see:
+ * a block, slot or position outside its range is skipped and recorded as
+ * S2ATTN_ERR_DEVICE_BOUNDS for s2attn_device_status(NULL, stream), in every
+ * build.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Blocks, slots and positions of the step's new tokens.  Request i has
+ * ctx_lens[i] tokens in the cache, in ceil(ctx/block_size) blocks, and gains
+ * new_lens[i] (negative lengths count as 0); the blocks it lacks are taken
+ * from free_blocks[0 .. num_free) in request order and written to its row of
+ * block_tables.  Writes
+ *   cu_seqlens [R + 1]  first token of each request, and the total;
+ *   positions  [T]      ctx + index in the request, or ctx + depth in a tree;
+ *   slots      [T]      the token's slot, -1 where no block is left for it
+ *                       (free list or table row used up; the table's entry is
+ *                       then -1 too, if it has one);
+ *   counts     [4]      blocks taken, blocks needed, total of new_lens, tokens
+ *                       left without a slot for want of a block.
+ * T is the length of positions and slots: entries behind the total get
+ * position 0, slot -1 and mask 0, tokens behind T are dropped (counts[2] > T),
+ * with the blocks only they would open.  parents (int32 [T], or NULL): the
+ * tokens of a request are a tree of drafts, parents[t] the index in the
+ * request of the draft before it, earlier than itself, or -1 (anything else
+ * counts as -1); mask (int64 [T], NULL exactly when parents is) then gets bit j
+ * for the token itself (index j) and each of its ancestors, as far as they are
+ * among the request's first 64.
+ * Any block_size; R * max_blocks and the sum of new_lens below 2^31.  No
+ * buffer may overlap another.  One launch.
+ */
+S2ATTN_API int s2attn_cache_plan(const int* ctx_lens, const int* new_lens, int* block_tables, const int* free_blocks,
+                                 const int* parents, int* cu_seqlens, int* positions, int* slots, int64_t* mask,
+                                 int* counts, int R, int max_blocks, int num_free, int block_size, int T,
+                                 s2attn_stream_t stream);
+
+/*
+ * Serving form of s2attn_qknorm_rope_fwd: token t of q [T, H, D], k and v
+ * [T, Hkv, D] is normed (w_q, w_k both NULL: not normed, eps is not used),
+ * rotated by row positions[t] of the table (table_rows rows) and written:
+ * q to q_out (may be q), k to k_cache and v (as it is) to v_cache at slots[t].
+ * A token with a negative slot is padding: its rows of q_out keep what they
+ * held, and so does the cache.  num_slots = num_blocks * block_size < 2^31.  Two
+ * tokens of one call must not share a slot.  One launch.
+ */
+S2ATTN_API int s2attn_cache_append(const void* q, const void* k, const void* v, const void* w_q, const void* w_k,
+                                   const float* table, const int* positions, const int* slots, void* q_out,
+                                   void* k_cache, void* v_cache, int T, int H, int Hkv, int D, int table_rows,
+                                   int64_t num_slots, int w_fp32, double eps, s2attn_stream_t stream);
+
+/* Workspace bytes of s2attn_cache_attn (0 for an unsupported head dim). */
+S2ATTN_API size_t s2attn_cache_attn_workspace_bytes(int D);
+
+/*
+ * Attention of the new tokens over the cache, their own keys already in it.
+ * Token j of request i (row cu_seqlens[i] + j of q [T, H, D]) attends the keys
+ * at places [0, ctx_lens[i]) and of the request's n new keys at places
+ * ctx + j' those with bit j' of its mask (int64 [T]; drafts past the 64th are
+ * seen by no token), or, where mask is NULL, those with j' <= j.  o: bf16
+ * [T, H, D]; lse: fp32 [H, T], natural log.  A row that sees no key gets o = 0
+ * and lse = -inf.  Rows of no request (behind cu_seqlens[R]) are left as they
+ * were.  Scale 1/sqrt(D); kv head of query head h is h / (H / Hkv).
+ * Keys in a block outside [0, num_blocks) count as zero vectors (and are
+ * recorded); places behind a row of block_tables do not exist.
+ * D in {64, 128}; block_size a power of two from 16 to 256; T H <= 2^30;
+ * num_blocks * block_size below 2^31, max_blocks * block_size at most 2^31 - 65536.
+ * workspace: 16-byte aligned, s2attn_cache_attn_workspace_bytes(D) bytes, need
+ * not be cleared; calls that overlap need one each.  Two launches; the result
+ * does not depend on timing.
+ */
+S2ATTN_API int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_tables,
+                                 const int* ctx_lens, const int* cu_seqlens, const int64_t* mask, void* o, float* lse,
+                                 int T, int R, int H, int Hkv, int D, int num_blocks, int block_size, int max_blocks,
+                                 void* workspace, size_t workspace_bytes, s2attn_stream_t stream);
+
 /*
  * Backward for callers that cannot allocate device memory (no counterpart in
  * the papers: this is a deployment variant of s2attn_bwd).  Some callers have
@@ -378,7 +498,9 @@ S2ATTN_API const char* s2attn_cuda_error_string(int err);
  * writes per-launch durations (ms) and kernel ids (0 forward, 1 backward
  * preprocess, 2 backward dK/dV, 3 backward dQ, 4 fused backward, 5 its dq
  * conversion, 6 RoPE rotation, 7 NF4 QKV projection, 8 NF4 dequantization, 9
- * backward dQ from the stored dS) to caller arrays of
+ * backward dQ from the stored dS, 10 query/key norm, 11 its backward, 12 its
+ * weight gradients, 13 cache append, 14 cache plan, 15 cache attention, 16 its
+ * join) to caller arrays of
  * `capacity` entries (either may be NULL).  Returns the number of records, or
  * minus a status code.
  */

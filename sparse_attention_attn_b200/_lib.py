@@ -61,6 +61,16 @@ SIGNATURES = {
     "s2attn_nf4_levels": (_i, [_vp]),
     "s2attn_nf4_qkv": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
     "s2attn_nf4_dequant": (_i, [_vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "s2attn_qknorm_rope_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, ctypes.c_double, _vp]),
+    "s2attn_qknorm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [_i]),
+    "s2attn_qknorm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                    ctypes.c_double, _vp, ctypes.c_size_t, _vp]),
+    "s2attn_cache_plan": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "s2attn_cache_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                 ctypes.c_int64, _i, ctypes.c_double, _vp]),
+    "s2attn_cache_attn_workspace_bytes": (ctypes.c_size_t, [_i]),
+    "s2attn_cache_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp,
+                               ctypes.c_size_t, _vp]),
     "s2attn_bwd_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                 _vp]),
 }
@@ -214,6 +224,42 @@ def s2attn_nf4_qkv(x, codes, scale_codes, c2, q, k, v, M, K, H, Hkv, D, stream) 
 
 def s2attn_nf4_dequant(codes, scale_codes, c2, w, rows, K, stream) -> int:
     return load().s2attn_nf4_dequant(codes, scale_codes, c2, w, rows, K, stream)
+
+
+def s2attn_qknorm_rope_fwd(q, k, w_q, w_k, table, q_out, k_out, B, N, H, Hkv, D, w_fp32, eps, stream) -> int:
+    return load().s2attn_qknorm_rope_fwd(q, k, w_q, w_k, table, q_out, k_out, B, N, H, Hkv, D, w_fp32, eps, stream)
+
+
+def s2attn_qknorm_rope_bwd_workspace_bytes(D) -> int:
+    return load().s2attn_qknorm_rope_bwd_workspace_bytes(D)
+
+
+def s2attn_qknorm_rope_bwd(q, k, w_q, w_k, table, dq_out, dk_out, dq, dk, dw_q, dw_k, B, N, H, Hkv, D, w_fp32, eps,
+                           workspace, workspace_bytes, stream) -> int:
+    return load().s2attn_qknorm_rope_bwd(q, k, w_q, w_k, table, dq_out, dk_out, dq, dk, dw_q, dw_k, B, N, H, Hkv, D,
+                                         w_fp32, eps, workspace, workspace_bytes, stream)
+
+
+def s2attn_cache_plan(ctx_lens, new_lens, block_tables, free_blocks, parents, cu_seqlens, positions, slots, mask,
+                      counts, R, max_blocks, num_free, block_size, T, stream) -> int:
+    return load().s2attn_cache_plan(ctx_lens, new_lens, block_tables, free_blocks, parents, cu_seqlens, positions,
+                                    slots, mask, counts, R, max_blocks, num_free, block_size, T, stream)
+
+
+def s2attn_cache_append(q, k, v, w_q, w_k, table, positions, slots, q_out, k_cache, v_cache, T, H, Hkv, D,
+                        table_rows, num_slots, w_fp32, eps, stream) -> int:
+    return load().s2attn_cache_append(q, k, v, w_q, w_k, table, positions, slots, q_out, k_cache, v_cache, T, H, Hkv,
+                                      D, table_rows, num_slots, w_fp32, eps, stream)
+
+
+def s2attn_cache_attn_workspace_bytes(D) -> int:
+    return load().s2attn_cache_attn_workspace_bytes(D)
+
+
+def s2attn_cache_attn(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mask, o, lse, T, R, H, Hkv, D,
+                      num_blocks, block_size, max_blocks, workspace, workspace_bytes, stream) -> int:
+    return load().s2attn_cache_attn(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mask, o, lse, T, R, H,
+                                    Hkv, D, num_blocks, block_size, max_blocks, workspace, workspace_bytes, stream)
 
 
 def s2attn_set_tile_override(spec) -> int:

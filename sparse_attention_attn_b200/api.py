@@ -12,6 +12,8 @@ attention.  Training uses the shifted groups, inference the dense path.
 """
 from __future__ import annotations
 
+from typing import NamedTuple, Optional
+
 import torch
 
 from . import _lib
@@ -458,3 +460,256 @@ def nf4_dequantize(codes, scale_codes, c2, out=None):
                                      _stream(dev))
     _lib._check("s2attn_nf4_dequant", st)
     return out
+
+
+# ---------------------------------------------------------------- query/key norm with rotation
+
+def _need_norm_weights(w_q, w_k, D: int, dev) -> int:
+    """Checks the two [D] norm weights; 1 for fp32, 0 for bf16."""
+    dtype = getattr(w_q, "dtype", None)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"w_q must be a torch.float32 or torch.bfloat16 tensor, got {dtype}")
+    _need("w_q", w_q, (D,), dtype, device=dev)
+    _need("w_k", w_k, (D,), dtype, device=dev)
+    return int(dtype == torch.float32)
+
+
+def _need_table(table, D: int, dev, rows=None) -> int:
+    if not isinstance(table, torch.Tensor) or table.dim() != 3:
+        raise ValueError("table must be a [rows, D/2, 2] tensor (rope_table)")
+    _need("table", table, (table.shape[0] if rows is None else rows, D // 2, 2), torch.float32, device=dev)
+    return table.shape[0]
+
+
+def qknorm_rope_forward(q, k, w_q, w_k, table, eps: float = 1e-6, q_out=None, k_out=None):
+    """Root-mean-square norm of every query and key head, weighted by w_q and
+    w_k ([D], fp32 or bf16), and the rotation by the table, in one pass.
+    q [B, N, H, D], k [B, N, Hkv, D] bf16; any N.  Returns (q_out, k_out), which
+    s2attn_forward takes; q_out may be q and k_out may be k (in place)."""
+    B, N, H, Hkv, D = _dims(q, k)
+    _need("q", q, (B, N, H, D))
+    dev = q.device
+    _need("k", k, (B, N, Hkv, D), device=dev)
+    w32 = _need_norm_weights(w_q, w_k, D, dev)
+    _need_table(table, D, dev, N)
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    k_out = torch.empty_like(k) if k_out is None else k_out
+    _need("q_out", q_out, (B, N, H, D), device=dev)
+    _need("k_out", k_out, (B, N, Hkv, D), device=dev)
+    with torch.cuda.device(dev):
+        st = _lib.s2attn_qknorm_rope_fwd(q.data_ptr(), k.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), table.data_ptr(),
+                                         q_out.data_ptr(), k_out.data_ptr(), B, N, H, Hkv, D, w32, float(eps),
+                                         _stream(dev))
+    _lib._check("s2attn_qknorm_rope_fwd", st)
+    return q_out, k_out
+
+
+def qknorm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, table, eps: float = 1e-6, dq=None, dk=None, dw_q=None,
+                         dw_k=None, workspace=None):
+    """Backward of qknorm_rope_forward from its inputs and the gradients of its
+    outputs.  Returns (dq, dk, dw_q, dw_k); the weight gradients have the
+    weights' type.  dq may be dq_out and dk may be dk_out (in place)."""
+    B, N, H, Hkv, D = _dims(q, k)
+    _need("q", q, (B, N, H, D))
+    dev = q.device
+    _need("k", k, (B, N, Hkv, D), device=dev)
+    _need("dq_out", dq_out, (B, N, H, D), device=dev)
+    _need("dk_out", dk_out, (B, N, Hkv, D), device=dev)
+    w32 = _need_norm_weights(w_q, w_k, D, dev)
+    _need_table(table, D, dev, N)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dw_q = torch.empty_like(w_q) if dw_q is None else dw_q
+    dw_k = torch.empty_like(w_k) if dw_k is None else dw_k
+    _need("dq", dq, (B, N, H, D), device=dev)
+    _need("dk", dk, (B, N, Hkv, D), device=dev)
+    _need("dw_q", dw_q, (D,), w_q.dtype, device=dev)
+    _need("dw_k", dw_k, (D,), w_q.dtype, device=dev)
+    workspace, wsb = _workspace("s2attn_qknorm_rope_bwd", workspace, _lib.s2attn_qknorm_rope_bwd_workspace_bytes(D),
+                                dev)
+    with torch.cuda.device(dev):
+        st = _lib.s2attn_qknorm_rope_bwd(q.data_ptr(), k.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), table.data_ptr(),
+                                         dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                         dw_q.data_ptr(), dw_k.data_ptr(), B, N, H, Hkv, D, w32, float(eps),
+                                         workspace.data_ptr(), wsb, _stream(dev))
+    _lib._check("s2attn_qknorm_rope_bwd", st)
+    return dq, dk, dw_q, dw_k
+
+
+def _workspace(fn: str, workspace, need: int, dev):
+    """The caller's workspace checked, or a new one; and its size."""
+    if need == 0:
+        raise _lib.S2AttnError(fn, _lib.S2ATTN_ERR_UNSUPPORTED)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise _lib.S2AttnError(fn, _lib.S2ATTN_ERR_WORKSPACE)
+    return workspace, have
+
+
+class QKNormRope(torch.autograd.Function):
+    """Autograd wrapper of the query/key norm with rotation: gradients for q,
+    k and both norm weights."""
+
+    @staticmethod
+    def forward(ctx, q, k, w_q, w_k, table, eps=1e-6):
+        q_out, k_out = qknorm_rope_forward(q, k, w_q, w_k, table, eps)
+        ctx.save_for_backward(q, k, w_q, w_k, table)
+        ctx.eps = eps
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, w_q, w_k, table = ctx.saved_tensors
+        dq, dk, dw_q, dw_k = qknorm_rope_backward(q, k, w_q, w_k, dq_out.contiguous(), dk_out.contiguous(), table,
+                                                  ctx.eps)
+        return dq, dk, dw_q, dw_k, None, None
+
+
+def s2_qknorm_attn(q, k, v, w_q, w_k, group_size: int, table, eps: float = 1e-6):
+    """Shifted sparse attention on normed and rotated q and k, with autograd
+    (training path of layers with query/key norm)."""
+    q_rot, k_rot = QKNormRope.apply(q, k, w_q, w_k, table, eps)
+    return S2Attention.apply(q_rot, k_rot, v, group_size)
+
+
+# ---------------------------------------------------------------- decoding over a paged cache
+
+class CachePlan(NamedTuple):
+    """Where the new tokens of a step go (int32 CUDA tensors, mask int64)."""
+    cu_seqlens: torch.Tensor          # [R + 1] first token of each request, and the total
+    positions: torch.Tensor           # [T] position for the rotation
+    slots: torch.Tensor               # [T] slot in the cache, -1: none
+    mask: Optional[torch.Tensor]      # [T] visible drafts of a tree, None without parents
+    counts: torch.Tensor              # [4] blocks taken, needed, new tokens, tokens left without a block
+
+
+def _need_ints(name: str, t, shape, dev=None) -> None:
+    _need(name, t, shape, torch.int32, device=dev)
+
+
+def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, num_tokens: int, parents=None):
+    """Blocks, slots and positions for the new tokens of a ragged batch, on the
+    GPU.  ctx_lens, new_lens int32 [R]: tokens in the cache and tokens to add;
+    block_tables int32 [R, max_blocks]: the requests' blocks, extended in place
+    by blocks of free_blocks (int32, taken from its front in request order);
+    num_tokens: size of the token arrays, at least sum(new_lens).  parents
+    int32 [num_tokens]: the new tokens of each request are a tree of drafts,
+    parents[t] the index in the request of the draft before it, -1 for the
+    context.  Returns a CachePlan."""
+    if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
+        raise ValueError("ctx_lens must be an int32 tensor [R]")
+    R, T = ctx_lens.shape[0], int(num_tokens)
+    _need_ints("ctx_lens", ctx_lens, (R,))
+    dev = ctx_lens.device
+    _need_ints("new_lens", new_lens, (R,), dev)
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise ValueError("block_tables must be an int32 tensor [R, max_blocks]")
+    _need_ints("block_tables", block_tables, (R, block_tables.shape[1]), dev)
+    if not isinstance(free_blocks, torch.Tensor) or free_blocks.dim() != 1:
+        raise ValueError("free_blocks must be an int32 tensor [num_free]")
+    _need_ints("free_blocks", free_blocks, (free_blocks.shape[0],), dev)
+    if parents is not None:
+        _need_ints("parents", parents, (T,), dev)
+    if T <= 0:
+        raise _lib.S2AttnError("s2attn_cache_plan", _lib.S2ATTN_ERR_INVALID_ARG)
+    mask = None if parents is None else torch.empty(T, dtype=torch.int64, device=dev)
+    buf = torch.empty(2 * T + R + 5, dtype=torch.int32, device=dev)  # one allocation
+    positions, slots, cu_seqlens, counts = buf.split((T, T, R + 1, 4))
+    p = buf.data_ptr()
+    with torch.cuda.device(dev):
+        st = _lib.s2attn_cache_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
+                                    free_blocks.data_ptr(), None if parents is None else parents.data_ptr(),
+                                    p + 8 * T, p, p + 4 * T, None if mask is None else mask.data_ptr(),
+                                    p + 4 * (2 * T + R + 1), R, block_tables.shape[1], free_blocks.shape[0],
+                                    int(block_size), T, _stream(dev))
+    _lib._check("s2attn_cache_plan", st)
+    return CachePlan(cu_seqlens, positions, slots, mask, counts)
+
+
+def _need_cache(k_cache, v_cache, Hkv, D, dev):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [num_blocks, block_size, Hkv, D] tensor")
+    nb, bs = k_cache.shape[:2]
+    if Hkv is None:
+        Hkv = k_cache.shape[2]
+    _need("k_cache", k_cache, (nb, bs, Hkv, D), device=dev)
+    _need("v_cache", v_cache, (nb, bs, Hkv, D), device=dev)
+    return nb, bs, Hkv
+
+
+def cache_append(q, k, v, table, positions, slots, k_cache, v_cache, w_q=None, w_k=None, eps: float = 1e-6,
+                 q_out=None):
+    """The serving form of qknorm_rope_forward: q [T, H, D], k and v
+    [T, Hkv, D] bf16, the new tokens of a ragged batch, are rotated by the
+    table's rows at positions (int32 [T]) -- after the norm where w_q and w_k
+    are given -- and k and v written to the caches ([num_blocks, block_size,
+    Hkv, D] bf16) at slots (int32 [T]).  Tokens with a negative slot are
+    padding: nothing is written for them.  No two tokens may share a slot.
+    Returns q_out (may be q)."""
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, H, D] and k [T, Hkv, D]")
+    T, H, D = q.shape
+    Hkv = k.shape[1]
+    _need("q", q, (T, H, D))
+    dev = q.device
+    _need("k", k, (T, Hkv, D), device=dev)
+    _need("v", v, (T, Hkv, D), device=dev)
+    _need_ints("positions", positions, (T,), dev)
+    _need_ints("slots", slots, (T,), dev)
+    nb, bs, _ = _need_cache(k_cache, v_cache, Hkv, D, dev)
+    rows = _need_table(table, D, dev)
+    if (w_q is None) != (w_k is None):
+        raise ValueError("w_q and w_k go together")
+    w32 = 0 if w_q is None else _need_norm_weights(w_q, w_k, D, dev)
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    _need("q_out", q_out, (T, H, D), device=dev)
+    with torch.cuda.device(dev):
+        st = _lib.s2attn_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                      None if w_q is None else w_q.data_ptr(),
+                                      None if w_k is None else w_k.data_ptr(), table.data_ptr(),
+                                      positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+                                      v_cache.data_ptr(), T, H, Hkv, D, rows, nb * bs, w32, float(eps), _stream(dev))
+    _lib._check("s2attn_cache_append", st)
+    return q_out
+
+
+def cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mask=None, out=None, lse=None,
+                    workspace=None):
+    """Attention of the new tokens of a ragged batch over a paged cache that
+    already holds their keys and values.  q [T, H, D] bf16; request i owns rows
+    cu_seqlens[i] .. cu_seqlens[i+1] of q (int32 [R + 1]), has ctx_lens[i]
+    earlier keys (int32 [R]) and the blocks of row i of block_tables (int32
+    [R, max_blocks]).  Every row attends the earlier keys and, of the request's
+    new ones, those its mask (int64 [T], bit j = new token j) names -- without
+    mask those up to its own.  Returns (o [T, H, D] bf16, lse [H, T] fp32); rows
+    that see no key get 0 and -inf, rows of no request are left as they are."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, H, D] tensor")
+    T, H, D = q.shape
+    _need("q", q, (T, H, D))
+    dev = q.device
+    nb, bs, Hkv = _need_cache(k_cache, v_cache, None, D, dev)
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise ValueError("block_tables must be an int32 tensor [R, max_blocks]")
+    R, maxb = block_tables.shape
+    _need_ints("block_tables", block_tables, (R, maxb), dev)
+    _need_ints("ctx_lens", ctx_lens, (R,), dev)
+    _need_ints("cu_seqlens", cu_seqlens, (R + 1,), dev)
+    if mask is not None:
+        _need("mask", mask, (T,), torch.int64, device=dev)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((H, T), dtype=torch.float32, device=dev) if lse is None else lse
+    _need("out", out, (T, H, D), device=dev)
+    _need("lse", lse, (H, T), torch.float32, device=dev)
+    workspace, wsb = _workspace("s2attn_cache_attn", workspace, _lib.s2attn_cache_attn_workspace_bytes(D), dev)
+    with torch.cuda.device(dev):
+        st = _lib.s2attn_cache_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                                    ctx_lens.data_ptr(), cu_seqlens.data_ptr(),
+                                    None if mask is None else mask.data_ptr(), out.data_ptr(), lse.data_ptr(), T, R,
+                                    H, Hkv, D, nb, bs, maxb, workspace.data_ptr(), wsb, _stream(dev))
+    _lib._check("s2attn_cache_attn", st)
+    return out, lse

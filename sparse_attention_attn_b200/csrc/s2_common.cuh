@@ -438,6 +438,77 @@ cudaError_t launch_nf4_qkv(const CUtensorMap& tx, const CUtensorMap& tc, const C
 cudaError_t launch_nf4_dequant(const void* codes, const int8_t* sq, const float* c2, void* w, long long n_words,
                                const Nf4Levels& lv, int num_sms, cudaStream_t stream);
 
+// Bounds checks on indexes that come from the caller's device data (positions,
+// cache slots, block numbers), which the host cannot see: compiled into every
+// build.  An index outside [0, n) records status code 7 and the site; the
+// caller skips the access.
+__device__ __forceinline__ bool data_in_range(uint32_t* status, long long idx, long long n, uint32_t where) {
+  if (idx >= 0 && idx < n) return true;
+  if (status != nullptr && atomicCAS(status, 0u, kDevBounds) == 0u) status[1] = where;
+  return false;
+}
+
+// Query/key norm with rotation (training layout) and its backward.
+struct QkNormArgs {
+  const __nv_bfloat16 *q, *k;      // inputs [tokens, H, D], [tokens, Hkv, D]
+  const __nv_bfloat16 *gq, *gk;    // backward: gradients of the rotated q, k
+  __nv_bfloat16 *yq, *yk;          // forward: rotated q, k; backward: gradients of q, k
+  const void *wq, *wk;             // norm weights [D]
+  const float2* table;             // (cos, sin) [N][D/2]
+  float* partial;                  // backward: [blocks][2][D] partial weight gradients
+  void *dwq, *dwk;                 // backward: weight gradients [D]
+  int tokens, N, H, Hkv;           // tokens = B N
+  float eps;
+};
+constexpr int kQkNormMaxBlocks = 1024;  // blocks whose partial weight gradients the workspace holds
+
+// The serving form: rows of a ragged batch, keys and values into cache slots.
+struct CacheAppendArgs {
+  const __nv_bfloat16 *q, *k, *v;  // [T, H, D], [T, Hkv, D]
+  const void *wq, *wk;             // norm weights [D], null: rotation only
+  const float2* table;             // [table_rows][D/2]
+  const int *positions, *slots;    // [T]
+  __nv_bfloat16 *q_out, *k_cache, *v_cache;
+  int T, H, Hkv, table_rows;
+  long long num_slots;
+  float eps;
+  uint32_t* status;
+};
+
+// Blocks, slots, positions and ancestor masks of the new tokens of a batch.
+struct CachePlanArgs {
+  const int *ctx_lens, *new_lens;  // [R]
+  int* block_tables;               // [R, max_blocks], new entries written
+  const int* free_blocks;          // [num_free]
+  const int* parents;              // [T] or null
+  int *cu_seqlens, *positions, *slots, *counts;  // [R+1], [T], [T], [4]
+  unsigned long long* mask;        // [T] or null
+  int R, max_blocks, num_free, block_size, T;
+};
+
+// Attention of new tokens over a paged cache.
+struct CacheAttnArgs {
+  const __nv_bfloat16 *q, *k_cache, *v_cache;  // [T, H, D], [num_blocks, block_size, Hkv, D]
+  const int *block_tables, *ctx_lens, *cu_seqlens;  // [R, max_blocks], [R], [R+1]
+  const unsigned long long* mask;                   // [T] or null: chains
+  __nv_bfloat16* o;                                 // [T, H, D]
+  float* lse;                                       // [H, T]
+  int4* desc;                                       // [grid] items to join
+  float* partial;                                   // [2 grid][rows (D + 2)]
+  int T, R, H, Hkv, rep, num_blocks, bs_log2, max_blocks;
+  float scale_log2;
+  uint32_t* status;
+};
+constexpr int kCacheRows = 16;     // query rows of a tile (mma.sync kernel)
+constexpr int kCacheMinUnits = 2;  // key tiles a CTA takes at least
+constexpr int kCacheGrid = 296;    // CTAs at most (two an SM of 148), which the workspace is sized for
+
+cudaError_t launch_qknorm_fwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
+cudaError_t launch_qknorm_bwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_append(const CacheAppendArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_plan(const CachePlanArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int D, int grid, cudaStream_t stream);
+
 // Optional per-kernel timing (s2attn_profile_start / _stop): the launchers
 // bracket every kernel with these; they do nothing unless profiling is on.
 enum KernelId : int {
@@ -450,7 +521,14 @@ enum KernelId : int {
   kKernelRope = 6,
   kKernelNf4Qkv = 7,
   kKernelNf4Dequant = 8,
-  kKernelBwdDqDs = 9
+  kKernelBwdDqDs = 9,
+  kKernelQkNorm = 10,
+  kKernelQkNormBwd = 11,
+  kKernelQkNormDw = 12,
+  kKernelCacheAppend = 13,
+  kKernelCachePlan = 14,
+  kKernelCacheAttn = 15,
+  kKernelCacheMerge = 16
 };
 void prof_before(cudaStream_t stream, int kernel_id);
 void prof_after(cudaStream_t stream);

@@ -1,0 +1,401 @@
+// Root-mean-square norm of every query and key head with a learned weight,
+// and the rotation by position, in one pass; its backward; and the serving
+// form, which takes the new tokens of a ragged batch at any positions and puts
+// the rotated keys and the values into their slots of a paged cache.
+//
+// For a head row x of D values at position t:
+//   r = 1 / sqrt(mean(x^2) + eps),  u = r x w,  y = R(a_t) u
+// with R the rotation of the pairs (i, i + D/2) by the table's (cos, sin).
+// Backward, from dy:  du = R(-a_t) dy,  dw = sum over rows of du r x,
+//   g = du w,  dx = r (g - r^2 x mean(g x)).
+// The row statistic is recomputed from x, so the forward stores nothing
+// besides y.  All arithmetic is fp32; y, dx and (for bf16 weights) dw are
+// rounded once.
+//
+// Every kernel is bound by HBM bytes at size (4 bytes a value forward, 6
+// backward).  D/16 lanes hold one row -- 8 values of each half per lane, so a
+// rotation pair never leaves its thread -- and reduce the row's sum by
+// shuffles; a thread walks a group of heads of one token with the token's 8
+// (cos, sin) pairs in registers.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "s2_common.cuh"
+#include "s2_ptx.cuh"
+
+namespace s2 {
+
+namespace {
+
+// 8 weights of one half at w + off, as fp32.
+__device__ __forceinline__ void load_w8(const float* w, int off, float (&o)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(w + off), b = *reinterpret_cast<const float4*>(w + off + 4);
+  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float (&o)[8]) {
+  const uint32_t p[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&p[j]));
+    o[2 * j] = f.x;
+    o[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void load_w8(const __nv_bfloat16* w, int off, float (&o)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(w + off), o);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void load_turn(const float2* table, size_t off, float (&c)[8], float (&s)[8]) {
+  const float4* tp = reinterpret_cast<const float4*>(table + off);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = tp[j];
+    c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
+  }
+}
+
+// Sum over the CH (4 or 8) lanes of a row; all 32 lanes of the warp take part.
+template <int CH>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int m = CH / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+// y = R(a) (r x w) of one lane's two octets; NORM false: r x w = x.
+template <int D, bool NORM>
+__device__ __forceinline__ void norm_rope_row(const uint4& u1, const uint4& u2, const float (&w1)[8],
+                                              const float (&w2)[8], const float (&c)[8], const float (&s)[8],
+                                              float eps, uint4& o1, uint4& o2) {
+  float x1[8], x2[8], y1[8], y2[8];
+  unpack8(u1, x1);
+  unpack8(u2, x2);
+  if (NORM) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x1[j], x1[j], fmaf(x2[j], x2[j], ss));
+    const float r = rsqrtf(row_sum<D / 16>(ss) * (1.f / D) + eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x1[j] *= r * w1[j];
+      x2[j] *= r * w2[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y1[j] = fmaf(x1[j], c[j], -x2[j] * s[j]);
+    y2[j] = fmaf(x1[j], s[j], x2[j] * c[j]);
+  }
+  o1 = pack8(y1);
+  o2 = pack8(y2);
+}
+
+// Forward.  A unit is a group of HG heads of one token (the query groups, then
+// the key groups); D/16 lanes take one unit.  Loops run on whole warps so that
+// the shuffles always have all lanes.
+template <int D, typename W, int HG>
+__global__ void __launch_bounds__(256) s2_qknorm_fwd_kernel(QkNormArgs a) {
+  constexpr int CH = D / 16;
+  const int gq = (a.H + HG - 1) / HG, gk = (a.Hkv + HG - 1) / HG, G = gq + gk;
+  const long long n = static_cast<long long>(a.tokens) * G * CH;
+  for (long long e0 = blockIdx.x * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += gridDim.x * 256LL) {
+    const long long e = e0 + (threadIdx.x & 31u);
+    const bool live = e < n;
+    const int ch = static_cast<int>(e % CH);
+    const uint32_t unit = live ? static_cast<uint32_t>(e / CH) : 0u;  // < 2^31 (checked by the host)
+    const int tok = unit / G, gi = unit - tok * G;
+    const bool is_q = gi < gq;
+    const int h0 = (is_q ? gi : gi - gq) * HG, heads = is_q ? a.H : a.Hkv;
+    const __nv_bfloat16* src = (is_q ? a.q : a.k) + (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
+    __nv_bfloat16* dst = (is_q ? a.yq : a.yk) + (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
+    uint4 u1[HG], u2[HG];
+#pragma unroll
+    for (int k = 0; k < HG; ++k) {
+      u1[k] = u2[k] = make_uint4(0, 0, 0, 0);
+      if (live && h0 + k < heads) {
+        u1[k] = *reinterpret_cast<const uint4*>(src + k * D);
+        u2[k] = *reinterpret_cast<const uint4*>(src + k * D + D / 2);
+      }
+    }
+    float c[8], s[8], w1[8], w2[8];
+    load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s);
+    const W* w = static_cast<const W*>(is_q ? a.wq : a.wk);
+    load_w8(w, ch * 8, w1);
+    load_w8(w, ch * 8 + D / 2, w2);
+#pragma unroll
+    for (int k = 0; k < HG; ++k) {
+      uint4 o1, o2;
+      norm_rope_row<D, true>(u1[k], u2[k], w1, w2, c, s, a.eps, o1, o2);
+      if (live && h0 + k < heads) {
+        *reinterpret_cast<uint4*>(dst + k * D) = o1;
+        *reinterpret_cast<uint4*>(dst + k * D + D / 2) = o2;
+      }
+    }
+  }
+}
+
+// Backward.  The same units, the query rows and then the key rows, HG heads at
+// a time; a thread keeps the sums of du r x of its 16 columns in registers,
+// and the block leaves one partial row per weight in the workspace.
+template <int D, typename W, int HG>
+__global__ void __launch_bounds__(256) s2_qknorm_bwd_kernel(QkNormArgs a) {
+  constexpr int CH = D / 16;
+  __shared__ float red[8][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = lane % CH;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int heads = which ? a.Hkv : a.H;
+    const __nv_bfloat16* x = which ? a.k : a.q;
+    const __nv_bfloat16* dy = which ? a.gk : a.gq;
+    __nv_bfloat16* dx = which ? a.yk : a.yq;
+    const W* w = static_cast<const W*>(which ? a.wk : a.wq);
+    float w1[8], w2[8], acc1[8], acc2[8];
+    load_w8(w, ch * 8, w1);
+    load_w8(w, ch * 8 + D / 2, w2);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc1[j] = acc2[j] = 0.f;
+    const int G = (heads + HG - 1) / HG;
+    const long long n = static_cast<long long>(a.tokens) * G * CH;
+    for (long long e0 = blockIdx.x * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += gridDim.x * 256LL) {
+      const long long e = e0 + lane;
+      const bool live = e < n;
+      const uint32_t unit = live ? static_cast<uint32_t>(e / CH) : 0u;
+      const int tok = unit / G, h0 = (unit - tok * G) * HG;
+      const size_t off = (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
+      uint4 u1[HG], u2[HG], d1[HG], d2[HG];
+#pragma unroll
+      for (int k = 0; k < HG; ++k) {
+        u1[k] = u2[k] = d1[k] = d2[k] = make_uint4(0, 0, 0, 0);
+        if (live && h0 + k < heads) {
+          u1[k] = *reinterpret_cast<const uint4*>(x + off + k * D);
+          u2[k] = *reinterpret_cast<const uint4*>(x + off + k * D + D / 2);
+          d1[k] = *reinterpret_cast<const uint4*>(dy + off + k * D);
+          d2[k] = *reinterpret_cast<const uint4*>(dy + off + k * D + D / 2);
+        }
+      }
+      float c[8], s[8];
+      load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s);
+#pragma unroll
+      for (int k = 0; k < HG; ++k) {
+        float x1[8], x2[8], g1[8], g2[8];
+        unpack8(u1[k], x1);
+        unpack8(u2[k], x2);
+        unpack8(d1[k], g1);
+        unpack8(d2[k], g2);
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x1[j], x1[j], fmaf(x2[j], x2[j], ss));
+        const float r = rsqrtf(row_sum<CH>(ss) * (1.f / D) + a.eps);
+        float gx = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // du, then dw += du r x, g = du w, sum of g x
+          const float du1 = fmaf(g1[j], c[j], g2[j] * s[j]), du2 = fmaf(g2[j], c[j], -g1[j] * s[j]);
+          acc1[j] = fmaf(du1, r * x1[j], acc1[j]);
+          acc2[j] = fmaf(du2, r * x2[j], acc2[j]);
+          g1[j] = du1 * w1[j];
+          g2[j] = du2 * w2[j];
+          gx = fmaf(g1[j], x1[j], fmaf(g2[j], x2[j], gx));
+        }
+        const float m = row_sum<CH>(gx) * (1.f / D) * r * r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          g1[j] = r * fmaf(-m, x1[j], g1[j]);
+          g2[j] = r * fmaf(-m, x2[j], g2[j]);
+        }
+        if (live && h0 + k < heads) {
+          *reinterpret_cast<uint4*>(dx + off + k * D) = pack8(g1);
+          *reinterpret_cast<uint4*>(dx + off + k * D + D / 2) = pack8(g2);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // lanes of equal chunk, then the block's warps
+#pragma unroll
+      for (int m = CH; m < 32; m <<= 1) {
+        acc1[j] += __shfl_xor_sync(0xffffffffu, acc1[j], m);
+        acc2[j] += __shfl_xor_sync(0xffffffffu, acc2[j], m);
+      }
+    }
+    __syncthreads();  // red[] of the query pass has been read
+    if (lane < CH) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        red[warp][ch * 8 + j] = acc1[j];
+        red[warp][ch * 8 + D / 2 + j] = acc2[j];
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
+      a.partial[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + threadIdx.x] = t;
+    }
+  }
+}
+
+// Sums the blocks' partial weight gradients (in fp64, in block order within
+// each of the 32 strides, so a result does not depend on timing).
+__device__ __forceinline__ void store_w(float* p, int i, double v) { p[i] = static_cast<float>(v); }
+__device__ __forceinline__ void store_w(__nv_bfloat16* p, int i, double v) { p[i] = __double2bfloat16(v); }
+
+template <int D, typename W>
+__global__ void __launch_bounds__(1024) s2_qknorm_dw_kernel(QkNormArgs a, int blocks) {
+  __shared__ double red[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;  // column of [2][D]
+  double t = 0.0;
+  for (int b = warp; b < blocks; b += 32) t += a.partial[static_cast<size_t>(b) * 2 * D + col];
+  red[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0) {
+    t = 0.0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += red[i][lane];
+    store_w(static_cast<W*>(col < D ? a.dwq : a.dwk), col % D, t);
+  }
+}
+
+// Serving form.  Units of a token: its query groups, key groups and value
+// groups.  A token whose slot is negative is padding: nothing of it is
+// written.  Positions outside the table and slots outside the cache are
+// recorded in the device status and the token is skipped.
+template <int D, typename W, bool NORM, int HG>
+__global__ void __launch_bounds__(256) s2_cache_append_kernel(CacheAppendArgs a) {
+  constexpr int CH = D / 16;
+  const int gq = (a.H + HG - 1) / HG, gk = (a.Hkv + HG - 1) / HG, G = gq + 2 * gk;
+  const long long n = static_cast<long long>(a.T) * G * CH;
+  for (long long e0 = blockIdx.x * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += gridDim.x * 256LL) {
+    const long long e = e0 + (threadIdx.x & 31u);
+    bool live = e < n;
+    const int ch = static_cast<int>(e % CH);
+    const uint32_t unit = live ? static_cast<uint32_t>(e / CH) : 0u;
+    const int tok = unit / G, gi = unit - tok * G;
+    const int slot = a.slots[tok], pos = a.positions[tok];
+    live = live && slot >= 0 && data_in_range(a.status, slot, a.num_slots, 701) &&
+           data_in_range(a.status, pos, a.table_rows, 702);
+    const int kind = gi < gq ? 0 : (gi < gq + gk ? 1 : 2);  // q, k, v
+    const int h0 = (kind == 0 ? gi : (kind == 1 ? gi - gq : gi - gq - gk)) * HG, heads = kind == 0 ? a.H : a.Hkv;
+    const size_t from = (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
+    const size_t to = kind == 0 ? from : (static_cast<size_t>(live ? slot : 0) * heads + h0) * D + ch * 8;
+    const __nv_bfloat16* src = (kind == 0 ? a.q : (kind == 1 ? a.k : a.v)) + from;
+    __nv_bfloat16* dst = (kind == 0 ? a.q_out : (kind == 1 ? a.k_cache : a.v_cache)) + to;
+    uint4 u1[HG], u2[HG];
+#pragma unroll
+    for (int k = 0; k < HG; ++k) {
+      u1[k] = u2[k] = make_uint4(0, 0, 0, 0);
+      if (live && h0 + k < heads) {
+        u1[k] = *reinterpret_cast<const uint4*>(src + k * D);
+        u2[k] = *reinterpret_cast<const uint4*>(src + k * D + D / 2);
+      }
+    }
+    float c[8], s[8], w1[8], w2[8];
+    load_turn(a.table, static_cast<size_t>(live ? pos : 0) * (D / 2) + ch * 8, c, s);
+    if (NORM) {
+      const W* w = static_cast<const W*>(kind == 0 ? a.wq : a.wk);
+      load_w8(w, ch * 8, w1);
+      load_w8(w, ch * 8 + D / 2, w2);
+    }
+#pragma unroll
+    for (int k = 0; k < HG; ++k) {
+      uint4 o1, o2;
+      norm_rope_row<D, NORM>(u1[k], u2[k], w1, w2, c, s, a.eps, o1, o2);
+      if (live && h0 + k < heads) {
+        *reinterpret_cast<uint4*>(dst + k * D) = kind == 2 ? u1[k] : o1;
+        *reinterpret_cast<uint4*>(dst + k * D + D / 2) = kind == 2 ? u2[k] : o2;
+      }
+    }
+  }
+}
+
+// Blocks for n threads of work, at most `per_sm` an SM.
+int blocks_for(long long n, int num_sms, int per_sm) {
+  const long long b = (n + 255) / 256;
+  const long long cap = static_cast<long long>(num_sms) * per_sm;
+  return static_cast<int>(b < cap ? b : cap);
+}
+
+template <int D, typename W>
+void fwd_launch(const QkNormArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int HG = 4;
+  const long long n = static_cast<long long>(a.tokens) * ((a.H + HG - 1) / HG + (a.Hkv + HG - 1) / HG) * (D / 16);
+  s2_qknorm_fwd_kernel<D, W, HG><<<blocks_for(n, num_sms, 16), 256, 0, stream>>>(a);
+}
+
+template <int D, typename W>
+int bwd_launch(const QkNormArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int HG = 2;
+  const long long n = static_cast<long long>(a.tokens) * ((a.H + HG - 1) / HG) * (D / 16);
+  int blocks = blocks_for(n, num_sms, 4);
+  if (blocks > kQkNormMaxBlocks) blocks = kQkNormMaxBlocks;
+  s2_qknorm_bwd_kernel<D, W, HG><<<blocks, 256, 0, stream>>>(a);
+  return blocks;
+}
+
+template <int D, typename W>
+void append_launch(const CacheAppendArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int HG = 4;
+  const long long n = static_cast<long long>(a.T) * ((a.H + HG - 1) / HG + 2 * ((a.Hkv + HG - 1) / HG)) * (D / 16);
+  const int grid = blocks_for(n, num_sms, 16);
+  if (a.wq != nullptr)
+    s2_cache_append_kernel<D, W, true, HG><<<grid, 256, 0, stream>>>(a);
+  else
+    s2_cache_append_kernel<D, W, false, HG><<<grid, 256, 0, stream>>>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_qknorm_fwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream) {
+  prof_before(stream, kKernelQkNorm);
+  if (D == 64)
+    w_fp32 ? fwd_launch<64, float>(a, num_sms, stream) : fwd_launch<64, __nv_bfloat16>(a, num_sms, stream);
+  else
+    w_fp32 ? fwd_launch<128, float>(a, num_sms, stream) : fwd_launch<128, __nv_bfloat16>(a, num_sms, stream);
+  const cudaError_t e = cudaGetLastError();
+  prof_after(stream);
+  return e;
+}
+
+cudaError_t launch_qknorm_bwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream) {
+  prof_before(stream, kKernelQkNormBwd);
+  int blocks;
+  if (D == 64)
+    blocks = w_fp32 ? bwd_launch<64, float>(a, num_sms, stream) : bwd_launch<64, __nv_bfloat16>(a, num_sms, stream);
+  else
+    blocks = w_fp32 ? bwd_launch<128, float>(a, num_sms, stream) : bwd_launch<128, __nv_bfloat16>(a, num_sms, stream);
+  cudaError_t e = cudaGetLastError();
+  prof_after(stream);
+  if (e != cudaSuccess) return e;
+  prof_before(stream, kKernelQkNormDw);
+  if (D == 64) {
+    if (w_fp32)
+      s2_qknorm_dw_kernel<64, float><<<4, 1024, 0, stream>>>(a, blocks);
+    else
+      s2_qknorm_dw_kernel<64, __nv_bfloat16><<<4, 1024, 0, stream>>>(a, blocks);
+  } else {
+    if (w_fp32)
+      s2_qknorm_dw_kernel<128, float><<<8, 1024, 0, stream>>>(a, blocks);
+    else
+      s2_qknorm_dw_kernel<128, __nv_bfloat16><<<8, 1024, 0, stream>>>(a, blocks);
+  }
+  e = cudaGetLastError();
+  prof_after(stream);
+  return e;
+}
+
+cudaError_t launch_cache_append(const CacheAppendArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream) {
+  prof_before(stream, kKernelCacheAppend);
+  if (D == 64)
+    w_fp32 ? append_launch<64, float>(a, num_sms, stream) : append_launch<64, __nv_bfloat16>(a, num_sms, stream);
+  else
+    w_fp32 ? append_launch<128, float>(a, num_sms, stream) : append_launch<128, __nv_bfloat16>(a, num_sms, stream);
+  const cudaError_t e = cudaGetLastError();
+  prof_after(stream);
+  return e;
+}
+
+}  // namespace s2

@@ -872,6 +872,57 @@ int nf4_dq_warps() {
   return v == "12" && nf4_stages() == 5 ? 12 : 8;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Status of a launcher's result, with the launch count and the error kept.
+int launched(cudaError_t e, int launches) {
+  if (e != cudaSuccess) {
+    g_last_cuda_error = static_cast<int>(e);
+    return S2ATTN_ERR_CUDA;
+  }
+  g_last_launches = launches;
+  return S2ATTN_OK;
+}
+
+bool status_block(uint32_t** out) {
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_fwd_status);
+  if (e != cudaSuccess) g_last_cuda_error = static_cast<int>(e);
+  *out = static_cast<uint32_t*>(p);
+  return e == cudaSuccess;
+}
+
+// Shapes of the query/key norm: any number of tokens and heads.
+int validate_qknorm(int B, int N, int H, int Hkv, int D, double eps) {
+  if (B <= 0 || N <= 0 || H <= 0 || Hkv <= 0 || D <= 0) return S2ATTN_ERR_INVALID_ARG;
+  // eps keeps a row of zeros finite, so it must be a normal fp32 number
+  if (!(eps >= 1.17549435e-38) || !(eps <= 3.4e38)) return S2ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return S2ATTN_ERR_UNSUPPORTED;
+  // tokens and head rows are counted in 32 bits
+  if (static_cast<long long>(B) * N > 0x7fffffffLL / 2 ||
+      static_cast<long long>(B) * N > 0x7fffffffLL / (static_cast<long long>(H) + 2LL * Hkv))
+    return S2ATTN_ERR_UNSUPPORTED;
+  return S2ATTN_OK;
+}
+
+QkNormArgs qknorm_args(const void* q, const void* k, const void* w_q, const void* w_k, const float* table, void* yq,
+                       void* yk, int B, int N, int H, int Hkv, double eps) {
+  QkNormArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.wq = w_q;
+  a.wk = w_k;
+  a.table = reinterpret_cast<const float2*>(table);
+  a.yq = static_cast<__nv_bfloat16*>(yq);
+  a.yk = static_cast<__nv_bfloat16*>(yk);
+  a.tokens = B * N;
+  a.N = N;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.eps = static_cast<float>(eps);
+  return a;
+}
+
 int validate_nf4(int M, int K, int H, int Hkv, int D) {
   if (M <= 0 || K <= 0 || H <= 0 || Hkv <= 0 || D <= 0) return S2ATTN_ERR_INVALID_ARG;
   if (K % 64 != 0) return S2ATTN_ERR_UNSUPPORTED;
@@ -970,6 +1021,185 @@ int s2attn_nf4_qkv(const void* x, const void* codes, const int8_t* scale_codes, 
   }
   g_last_launches = 1;
   return S2ATTN_OK;
+}
+
+int s2attn_qknorm_rope_fwd(const void* q, const void* k, const void* w_q, const void* w_k, const float* table,
+                           void* q_out, void* k_out, int B, int N, int H, int Hkv, int D, int w_fp32, double eps,
+                           s2attn_stream_t stream) {
+  g_last_launches = 0;
+  if (!q || !k || !w_q || !w_k || !table || !q_out || !k_out) return S2ATTN_ERR_INVALID_ARG;
+  const int st = validate_qknorm(B, N, H, Hkv, D, eps);
+  if (st != S2ATTN_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(w_q) || !aligned16(w_k) || !aligned16(table) ||
+      !aligned16(q_out) || !aligned16(k_out))
+    return S2ATTN_ERR_MISALIGNED;
+  DeviceInfo info;
+  if (!device_info(&info)) return S2ATTN_ERR_CUDA;
+  if (!info.ok) return S2ATTN_ERR_UNSUPPORTED;
+  QkNormArgs a = qknorm_args(q, k, w_q, w_k, table, q_out, k_out, B, N, H, Hkv, eps);
+  return launched(launch_qknorm_fwd(a, D, w_fp32 ? 1 : 0, info.sms, static_cast<cudaStream_t>(stream)), 1);
+}
+
+size_t s2attn_qknorm_rope_bwd_workspace_bytes(int D) {
+  return D == 64 || D == 128 ? static_cast<size_t>(kQkNormMaxBlocks) * 2 * D * sizeof(float) : 0;
+}
+
+int s2attn_qknorm_rope_bwd(const void* q, const void* k, const void* w_q, const void* w_k, const float* table,
+                           const void* dq_out, const void* dk_out, void* dq, void* dk, void* dw_q, void* dw_k, int B,
+                           int N, int H, int Hkv, int D, int w_fp32, double eps, void* workspace,
+                           size_t workspace_bytes, s2attn_stream_t stream) {
+  g_last_launches = 0;
+  if (!q || !k || !w_q || !w_k || !table || !dq_out || !dk_out || !dq || !dk || !dw_q || !dw_k)
+    return S2ATTN_ERR_INVALID_ARG;
+  const int st = validate_qknorm(B, N, H, Hkv, D, eps);
+  if (st != S2ATTN_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(w_q) || !aligned16(w_k) || !aligned16(table) ||
+      !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dw_q) ||
+      !aligned16(dw_k))
+    return S2ATTN_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < s2attn_qknorm_rope_bwd_workspace_bytes(D) || !aligned16(workspace))
+    return S2ATTN_ERR_WORKSPACE;
+  DeviceInfo info;
+  if (!device_info(&info)) return S2ATTN_ERR_CUDA;
+  if (!info.ok) return S2ATTN_ERR_UNSUPPORTED;
+  QkNormArgs a = qknorm_args(q, k, w_q, w_k, table, dq, dk, B, N, H, Hkv, eps);
+  a.gq = static_cast<const __nv_bfloat16*>(dq_out);
+  a.gk = static_cast<const __nv_bfloat16*>(dk_out);
+  a.partial = static_cast<float*>(workspace);
+  a.dwq = dw_q;
+  a.dwk = dw_k;
+  return launched(launch_qknorm_bwd(a, D, w_fp32 ? 1 : 0, info.sms, static_cast<cudaStream_t>(stream)), 2);
+}
+
+int s2attn_cache_append(const void* q, const void* k, const void* v, const void* w_q, const void* w_k,
+                        const float* table, const int* positions, const int* slots, void* q_out, void* k_cache,
+                        void* v_cache, int T, int H, int Hkv, int D, int table_rows, int64_t num_slots, int w_fp32,
+                        double eps, s2attn_stream_t stream) {
+  g_last_launches = 0;
+  if (!q || !k || !v || !table || !positions || !slots || !q_out || !k_cache || !v_cache)
+    return S2ATTN_ERR_INVALID_ARG;
+  if ((w_q == nullptr) != (w_k == nullptr) || table_rows <= 0 || num_slots <= 0) return S2ATTN_ERR_INVALID_ARG;
+  const int st = validate_qknorm(1, T, H, Hkv, D, w_q ? eps : 1.0);
+  if (st != S2ATTN_OK) return st;
+  if (num_slots > 0x7fffffffLL) return S2ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(w_q) || !aligned16(w_k) || !aligned16(table) ||
+      !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(positions) || !aligned4(slots))
+    return S2ATTN_ERR_MISALIGNED;
+  DeviceInfo info;
+  if (!device_info(&info)) return S2ATTN_ERR_CUDA;
+  if (!info.ok) return S2ATTN_ERR_UNSUPPORTED;
+  CacheAppendArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.wq = w_q;
+  a.wk = w_k;
+  a.table = reinterpret_cast<const float2*>(table);
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  a.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.table_rows = table_rows;
+  a.num_slots = num_slots;
+  a.eps = static_cast<float>(eps);
+  if (!status_block(&a.status)) return S2ATTN_ERR_CUDA;
+  return launched(launch_cache_append(a, D, w_fp32 ? 1 : 0, info.sms, static_cast<cudaStream_t>(stream)), 1);
+}
+
+int s2attn_cache_plan(const int* ctx_lens, const int* new_lens, int* block_tables, const int* free_blocks,
+                      const int* parents, int* cu_seqlens, int* positions, int* slots, int64_t* mask, int* counts,
+                      int R, int max_blocks, int num_free, int block_size, int T, s2attn_stream_t stream) {
+  g_last_launches = 0;
+  if (!ctx_lens || !new_lens || !block_tables || !cu_seqlens || !positions || !slots || !counts)
+    return S2ATTN_ERR_INVALID_ARG;
+  if (R <= 0 || max_blocks <= 0 || num_free < 0 || block_size <= 0 || T <= 0) return S2ATTN_ERR_INVALID_ARG;
+  if ((num_free > 0 && !free_blocks) || (parents == nullptr) != (mask == nullptr)) return S2ATTN_ERR_INVALID_ARG;
+  // the scan counts new blocks in 32 bits; a request has at most max_blocks of them
+  if (static_cast<int64_t>(R) * max_blocks > 0x7fffffffLL) return S2ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(ctx_lens) || !aligned4(new_lens) || !aligned4(block_tables) || !aligned4(free_blocks) ||
+      !aligned4(parents) || !aligned4(cu_seqlens) || !aligned4(positions) || !aligned4(slots) || !aligned4(counts) ||
+      (reinterpret_cast<uintptr_t>(mask) & 7u) != 0)
+    return S2ATTN_ERR_MISALIGNED;
+  DeviceInfo info;
+  if (!device_info(&info)) return S2ATTN_ERR_CUDA;
+  if (!info.ok) return S2ATTN_ERR_UNSUPPORTED;
+  CachePlanArgs a;
+  a.ctx_lens = ctx_lens;
+  a.new_lens = new_lens;
+  a.block_tables = block_tables;
+  a.free_blocks = free_blocks;
+  a.parents = parents;
+  a.cu_seqlens = cu_seqlens;
+  a.positions = positions;
+  a.slots = slots;
+  a.counts = counts;
+  a.mask = reinterpret_cast<unsigned long long*>(mask);
+  a.R = R;
+  a.max_blocks = max_blocks;
+  a.num_free = num_free;
+  a.block_size = block_size;
+  a.T = T;
+  return launched(launch_cache_plan(a, info.sms, static_cast<cudaStream_t>(stream)), 1);
+}
+
+size_t s2attn_cache_attn_workspace_bytes(int D) {
+  if (D != 64 && D != 128) return 0;
+  return static_cast<size_t>(kCacheGrid) * (sizeof(int4) + 2 * kCacheRows * (D + 2) * sizeof(float));
+}
+
+int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_tables,
+                      const int* ctx_lens, const int* cu_seqlens, const int64_t* mask, void* o, float* lse, int T,
+                      int R, int H, int Hkv, int D, int num_blocks, int block_size, int max_blocks, void* workspace,
+                      size_t workspace_bytes, s2attn_stream_t stream) {
+  g_last_launches = 0;
+  if (!q || !k_cache || !v_cache || !block_tables || !ctx_lens || !cu_seqlens || !o || !lse)
+    return S2ATTN_ERR_INVALID_ARG;
+  if (T <= 0 || R <= 0 || H <= 0 || Hkv <= 0 || D <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks <= 0)
+    return S2ATTN_ERR_INVALID_ARG;
+  if (H % Hkv != 0) return S2ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return S2ATTN_ERR_UNSUPPORTED;
+  if (block_size < 16 || block_size > 256 || (block_size & (block_size - 1)) != 0) return S2ATTN_ERR_UNSUPPORTED;
+  // rows, places and keys are 32-bit numbers in the kernel
+  if (static_cast<int64_t>(T) * H > (1LL << 30) || static_cast<int64_t>(num_blocks) * block_size > 0x7fffffffLL ||
+      static_cast<int64_t>(max_blocks) * block_size > 0x7fffffffLL - 65536 || R > (1 << 24))
+    return S2ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned4(lse) ||
+      !aligned4(block_tables) || !aligned4(ctx_lens) || !aligned4(cu_seqlens) ||
+      (reinterpret_cast<uintptr_t>(mask) & 7u) != 0)
+    return S2ATTN_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < s2attn_cache_attn_workspace_bytes(D) || !aligned16(workspace))
+    return S2ATTN_ERR_WORKSPACE;
+  DeviceInfo info;
+  if (!device_info(&info)) return S2ATTN_ERR_CUDA;
+  if (!info.ok) return S2ATTN_ERR_UNSUPPORTED;
+  CacheAttnArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
+  a.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
+  a.block_tables = block_tables;
+  a.ctx_lens = ctx_lens;
+  a.cu_seqlens = cu_seqlens;
+  a.mask = reinterpret_cast<const unsigned long long*>(mask);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.desc = static_cast<int4*>(workspace);
+  a.partial = reinterpret_cast<float*>(a.desc + kCacheGrid);
+  a.T = T;
+  a.R = R;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.rep = H / Hkv;
+  a.num_blocks = num_blocks;
+  a.bs_log2 = __builtin_ctz(static_cast<unsigned>(block_size));
+  a.max_blocks = max_blocks;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(D)));
+  if (!status_block(&a.status)) return S2ATTN_ERR_CUDA;
+  const int grid = 2 * info.sms < kCacheGrid ? 2 * info.sms : kCacheGrid;
+  return launched(launch_cache_attn(a, D, grid, static_cast<cudaStream_t>(stream)), 2);
 }
 
 size_t s2attn_hga_bwd_workspace_bytes(int B, int H, int Hkv, int N, int D, int G) {
