@@ -1,0 +1,713 @@
+// Attention of new tokens over a paged cache on the tensor cores (tcgen05,
+// TMEM accumulators, TMA-fed rings): one token, a chain or a tree of drafts for
+// each request of a ragged batch.
+//
+//   o = softmax(q K^T / sqrt(D), masked) V,  lse = log sum exp (natural log)
+//
+// Token j of request i (rows cu[i] .. cu[i+1]) sees every key before ctx_i and,
+// of the request's own new keys, those its mask names (bit j' = draft j'), or
+// without masks the drafts up to itself.  Key p of request i is row p % bs of
+// cache block block_table[i][p / bs].
+//
+// Rows.  The rep = H/Hkv query heads that share a kv head form one 128-row tile
+// with floor(128 / rep) tokens: row = token * rep + head in group, which is the
+// order a {64 columns, rep heads, tokens} TMA box lands in shared memory.  An
+// item is two adjacent tiles (A, B) of one (request, kv head).
+//
+// Split.  A unit is 128 keys of one item; all units of a batch are numbered
+// request by request and dealt to the CTAs (one per SM) in equal contiguous
+// runs, so that a batch of very different lengths, or one long request, loads
+// every SM alike.  A run that covers only part of an item's keys (a segment)
+// leaves unnormalised sums, row maxima and row sums in the workspace, and a
+// second kernel joins the parts in order: the split depends on the lengths
+// alone, so the same call gives the same bits.
+//
+// Two ways through a segment keep both softmax warpgroups and the tensor core
+// busy.  Paired (the item has tile B): every key tile feeds both query tiles,
+// one load for 256 rows.  Alternating (few rows, tile A alone): warpgroup A
+// takes the even and warpgroup B the odd key tiles of the same query tile, and
+// A joins the two accumulators from TMEM at the end.  With few rows the kernel
+// is bound by reading the cache; the padding of the 128-row tile is free there
+// (1024 tensor cycles a 64 KB tile against some 2800 of HBM time).
+//
+// Warp roles (320 threads): warp 0 TMA producer (Q ring, K/V ring, the pages of
+// a tile loaded by one lane each), warp 1 UMMA issuer, warps 2-5 softmax A,
+// warps 6-9 softmax B, one thread per query row.  P is rounded to bf16 for the
+// product with V; its row sums, the maxima and O stay fp32.  Rows of V behind
+// the last key may hold anything (stale cache rows): the product stops at the
+// 16-key step that holds the last key, and the rows of that step behind it are
+// zeroed in shared memory first.
+//
+// TMEM (512 columns): S_A [0,128), S_B [128,256) (P over their first 64
+// columns), O_A [256, 256+D), O_B [384, 384+D).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "s2_common.cuh"
+#include "s2_ptx.cuh"
+
+namespace s2 {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr float kFloor = -3.0e38f;  // running maximum of a row that has seen no key (finite: no inf - inf)
+
+template <int D>
+struct TcCfg {
+  static constexpr int NQ = D == 128 ? 3 : 4;       // Q ring
+  static constexpr int NS = D == 128 ? 4 : 8;       // K/V ring
+  static constexpr int ATOM = kTile * 128;          // one 64-column slab of a 128-row tile
+  static constexpr int TILE = kTile * D * 2;
+  static constexpr int OFF_KV = NQ * TILE;
+  static constexpr int SMEM = OFF_KV + NS * TILE + 1024;
+  static constexpr uint32_t TM_O = 256, TM_OB = 384;
+  static_assert(SMEM <= 232448 - 2048, "shared memory");
+};
+
+// The lengths of request i, and its units.
+struct Req {
+  int ctx, n, row0;  // cached tokens, new tokens, first row of q
+  int keys;          // keys in all
+  int kt, np;        // key tiles, items a kv head
+  long long units;   // Hkv * np * kt
+};
+__device__ __forceinline__ Req request(const CacheAttnArgs& a, int i) {
+  Req r;
+  r.row0 = min(max(a.cu_seqlens[i], 0), a.T);
+  const int end = min(max(a.cu_seqlens[i + 1], r.row0), a.T);
+  r.n = end - r.row0;
+  const long long most = static_cast<long long>(a.max_blocks) << a.bs_log2;  // places the table has
+  r.ctx = static_cast<int>(min(static_cast<long long>(max(a.ctx_lens[i], 0)), most));
+  r.keys = static_cast<int>(min(static_cast<long long>(r.ctx) + r.n, most));
+  r.kt = (r.keys + kTile - 1) / kTile;
+  r.np = (r.n + 2 * a.tpt - 1) / (2 * a.tpt);
+  r.units = static_cast<long long>(a.Hkv) * r.np * r.kt;
+  return r;
+}
+
+// A CTA's run of units and the walk through its segments.
+struct Run {
+  long long u0, u1, rbase;  // units of the run; first unit of request ri
+  int ri;
+};
+struct Seg {
+  int ri, kvh;
+  int row0, n, ctx, keys;  // the request (row0: first row of q)
+  int tok;                 // first token of tile A in the request
+  int na, nb;              // tokens of tiles A and B (nb = 0: alternating)
+  int kt0, tiles;          // first key tile, key tiles to work on (0: none is visible)
+  int whole, first;        // the whole item; the part with key tile 0
+  int last_cta;            // first && !whole: CTA with the item's last part
+};
+__device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, Run& w, long long per, Seg& s) {
+  while (w.u0 < w.u1) {
+    const Req r = request(a, w.ri);
+    if (w.u0 >= w.rbase + r.units) {
+      w.rbase += r.units;
+      ++w.ri;
+      continue;
+    }
+    const long long in = w.u0 - w.rbase, item = in / r.kt;  // item = kvh * np + pair
+    const int pair = static_cast<int>(item % r.np);
+    s.ri = w.ri;
+    s.kvh = static_cast<int>(item / r.np);
+    s.row0 = r.row0;
+    s.n = r.n;
+    s.ctx = r.ctx;
+    s.keys = r.keys;
+    s.tok = pair * 2 * a.tpt;
+    s.na = min(a.tpt, r.n - s.tok);
+    s.nb = min(a.tpt, r.n - s.tok - s.na);
+    s.kt0 = static_cast<int>(in - item * r.kt);
+    const int kt1 = static_cast<int>(min(static_cast<long long>(r.kt), s.kt0 + (w.u1 - w.u0)));
+    // chains: keys behind the item's last token are not visited
+    const int reach = a.mask != nullptr ? r.keys : min(r.ctx + min(s.tok + s.na + s.nb, r.keys - r.ctx), r.keys);
+    s.tiles = max(min(kt1, (reach + kTile - 1) / kTile) - s.kt0, 0);
+    s.first = s.kt0 == 0;
+    s.whole = s.first && kt1 == r.kt;
+    s.last_cta = static_cast<int>((w.rbase + (item + 1) * r.kt - 1) / per);
+    w.u0 += kt1 - s.kt0;
+    return true;
+  }
+  return false;
+}
+
+// Sum of v over the block; every thread gets it.
+__device__ __forceinline__ long long block_sum(long long v, long long* buf) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += buf[w];
+  return v;
+}
+
+__device__ __forceinline__ size_t part_floats(int D) { return static_cast<size_t>(2 * kTile) * (D + 2); }
+
+// acc (bit patterns, 32 columns from c0 of one row) out: o normalised, or the partial as it is.
+__device__ __forceinline__ void store_o32(__nv_bfloat16* o, float* part, bool whole, const uint32_t (&v)[32], float inv) {
+  if (whole) {
+    store_row32(o, v, inv);
+  } else {
+    uint4* p = reinterpret_cast<uint4*>(part);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) p[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    s2_cache_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a) {
+  using C = TcCfg<D>;
+  constexpr int NQ = C::NQ, NS = C::NS;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t bar_qfull[NQ], bar_qempty[NQ], bar_full[NS], bar_empty[NS], bar_s[2], bar_plo[2],
+      bar_p[2], bar_o[2], bar_ofree[2], bar_mb, bar_drain;
+  __shared__ uint32_t tmem_slot, abort_flag;
+  __shared__ long long sums[kThreads / 32], found_before;
+  __shared__ int found;
+  __shared__ float b_m[kTile], b_l[kTile];  // alternating: warpgroup B's row maxima and sums
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // ---- the run of units of this CTA and the request it begins in
+  long long total = 0;
+  for (int base = 0; base < a.R; base += kThreads) {
+    const int i = base + tid;
+    total += block_sum(i < a.R ? request(a, i).units : 0, sums);
+  }
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, 1LL);
+  Run run;
+  run.u0 = per * blockIdx.x;
+  run.u1 = min(run.u0 + per, total);
+  if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (run.u0 >= run.u1) return;
+  long long before = 0;
+  for (int base = 0; base < a.R; base += kThreads) {
+    const int i = base + tid;
+    const long long mine = i < a.R ? request(a, i).units : 0;
+    long long inc = mine;  // inclusive scan of the chunk
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+      if (lane >= m) inc += o;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    long long all = 0, mybase = before;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) mybase += sums[w];
+      all += sums[w];
+    }
+    if (run.u0 >= mybase + inc - mine && run.u0 < mybase + inc) {
+      found = i;
+      found_before = mybase + inc - mine;
+    }
+    before += all;
+    if (run.u0 < before) break;  // uniform
+  }
+  WaitCtx wc{&abort_flag, a.status, a.wait_limit_ns};
+  const uint32_t sQ = smem_u32(smem);
+  auto q_addr = [&](int s) { return sQ + s * C::TILE; };
+  auto kv_addr = [&](int s) { return sQ + C::OFF_KV + s * C::TILE; };
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(smem_u32(&bar_qfull[s]), 1);
+      mbar_init(smem_u32(&bar_qempty[s]), 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bar_s[i]), 1);
+      mbar_init(smem_u32(&bar_plo[i]), 4);
+      mbar_init(smem_u32(&bar_p[i]), 4);
+      mbar_init(smem_u32(&bar_o[i]), 1);
+      mbar_init(smem_u32(&bar_ofree[i]), 4);
+    }
+    mbar_init(smem_u32(&bar_mb), 4);
+    mbar_init(smem_u32(&bar_drain), 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  run.ri = found;
+  run.rbase = found_before;
+  Seg sg;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (elect_one()) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    __syncwarp();
+    int qu = 0, L = 0;  // ring uses so far
+    bool ok = true;
+    const int page_rows = min(1 << a.bs_log2, kTile), page_log2 = min(a.bs_log2, 7);
+    auto load_q = [&](int token) -> bool {
+      const int s = qu % NQ, r = qu / NQ;
+      if (r > 0 && !warp_wait(smem_u32(&bar_qempty[s]), (r - 1) & 1, wc, 110)) return false;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(smem_u32(&bar_qfull[s]), a.tpt * a.rep * 128 * (D / 64));
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(q_addr(s) + c * C::ATOM, &tmQ, smem_u32(&bar_qfull[s]), c * 64, sg.kvh * a.rep, token, 0);
+      }
+      __syncwarp();
+      ++qu;
+      return true;
+    };
+    // one lane per page; a block outside the cache reads as zeros (its row lies behind the tensor)
+    auto load_kv = [&](const CUtensorMap* map, bool mine, int row) -> bool {
+      const int s = L % NS, r = L / NS;
+      if (r > 0 && !warp_wait(smem_u32(&bar_empty[s]), (r - 1) & 1, wc, 111)) return false;
+      const int pages = __popc(__ballot_sync(0xffffffffu, mine));
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar_full[s]), pages * page_rows * 128 * (D / 64));
+      __syncwarp();
+      if (mine)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(kv_addr(s) + c * C::ATOM + (lane << page_log2) * 128, map, smem_u32(&bar_full[s]), c * 64, sg.kvh,
+                      row, 0);
+      __syncwarp();
+      ++L;
+      return true;
+    };
+    while (ok && next_segment(a, run, per, sg)) {
+      if (sg.tiles == 0) continue;
+      ok = load_q(sg.row0 + sg.tok) && (sg.nb == 0 || load_q(sg.row0 + sg.tok + a.tpt));
+      const int* table = a.block_tables + static_cast<size_t>(sg.ri) * a.max_blocks;
+      for (int i = 0; ok && i < sg.tiles; ++i) {
+        const int key = (sg.kt0 + i) * kTile + (lane << page_log2);
+        const bool mine = lane < (kTile >> page_log2) && key < sg.keys;
+        int row = 0;
+        if (mine) {
+          const int blk = table[key >> a.bs_log2];
+          row = data_in_range(a.status, blk, a.num_blocks, 711) ? (blk << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))
+                                                                : a.num_blocks << a.bs_log2;
+        }
+        ok = load_kv(&tmK, mine, row) && load_kv(&tmV, mine, row);
+      }
+    }
+    if (*wc.abort && lane == 0) {
+      // never leave copies in flight into shared memory: wait (bounded) for
+      // the last fill of every slot
+      for (int s = 0; s < NQ && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / NQ) & 1);
+      for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ UMMA issuer
+    const uint32_t idS = make_idesc_bf16(128, kTile, 0, 0);  // Q K-major, K K-major
+    const uint32_t idO = make_idesc_bf16(128, D, 0, 1);      // P from TMEM, V MN-major
+    const uint64_t dQ0 = make_sdesc_sw128(q_addr(0), 16, 1024);
+    const uint64_t dK0 = make_sdesc_sw128(kv_addr(0), 16, 1024);
+    const uint64_t dV0 = make_sdesc_sw128(kv_addr(0), C::ATOM, 1024);
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(smem_u32(bar));
+      __syncwarp();
+    };
+    auto wait_full = [&](int Lx) { return warp_wait(smem_u32(&bar_full[Lx % NS]), (Lx / NS) & 1, wc, 120); };
+    auto issue_s = [&](int wg, int qs, int Lk) {
+      tc_fence_after();
+      const uint64_t dq = sdesc_advance(dQ0, qs * C::TILE);
+      const uint64_t dk = sdesc_advance(dK0, (Lk % NS) * C::TILE);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::ATOM + (kk & 3) * 32;
+          umma_ss(tmem + wg * 128, sdesc_advance(dq, off), sdesc_advance(dk, off), idS, kk > 0);
+        }
+        umma_commit(smem_u32(&bar_s[wg]));
+      }
+      __syncwarp();
+    };
+    int L = 0, qu = 0, np[2] = {0, 0}, nseg[2] = {0, 0};
+    // O_wg (+)= P_wg V(load Lv) over the 16-key steps [k0, k1) of the tile
+    auto issue_pv = [&](int wg, int Lv, int k0, int k1, bool acc) {
+      tc_fence_after();
+      const uint64_t dv = sdesc_advance(dV0, (Lv % NS) * C::TILE);
+      if (elect_one())
+        for (int kk = k0; kk < k1; ++kk)
+          umma_ts(tmem + (wg ? C::TM_OB : C::TM_O), tmem + wg * 128 + kk * 8, sdesc_advance(dv, kk * 2048), idO,
+                  acc || kk > 0);
+      __syncwarp();
+    };
+    // step j of warpgroup wg: P V of key tile t, keys 0..63 as soon as they are there
+    auto pv = [&](int wg, int Lv, int j, int t) -> bool {
+      const int nk = (min(sg.keys - t * kTile, kTile) + 15) >> 4;  // 16-key steps with a key
+      if (!warp_wait(smem_u32(&bar_plo[wg]), np[wg] & 1, wc, 122 + wg)) return false;
+      if (j == 0 && nseg[wg] > 0 && !warp_wait(smem_u32(&bar_ofree[wg]), (nseg[wg] - 1) & 1, wc, 124 + wg)) return false;
+      if (!wait_full(Lv)) return false;
+      issue_pv(wg, Lv, 0, min(nk, 4), j > 0);
+      if (!warp_wait(smem_u32(&bar_p[wg]), np[wg] & 1, wc, 126 + wg)) return false;
+      issue_pv(wg, Lv, 4, nk, true);
+      commit(&bar_o[wg]);
+      ++np[wg];
+      return true;
+    };
+    bool ok = true;
+    while (ok && next_segment(a, run, per, sg)) {
+      if (sg.tiles == 0) continue;
+      const bool alt = sg.nb == 0;
+      const int n = sg.tiles, nA = alt ? (n + 1) / 2 : n, nB = alt ? n / 2 : n;
+      const int qa = qu % NQ, qb = alt ? qa : (qu + 1) % NQ, L0 = L;
+      // load of the K tile of step j (its V tile is the next load), and the key tile
+      auto lk = [&](int wg, int j) { return L0 + (alt ? 4 * j + 2 * wg : 2 * j); };
+      auto tile = [&](int wg, int j) { return sg.kt0 + (alt ? 2 * j + wg : j); };
+      ok = warp_wait(smem_u32(&bar_qfull[qa]), (qu / NQ) & 1, wc, 121) &&
+           (alt || warp_wait(smem_u32(&bar_qfull[qb]), ((qu + 1) / NQ) & 1, wc, 121)) && wait_full(lk(0, 0));
+      if (!ok) break;
+      issue_s(0, qa, lk(0, 0));
+      if (alt) commit(&bar_empty[lk(0, 0) % NS]);
+      if (nB > 0) {
+        if (alt && !(ok = wait_full(lk(1, 0)))) break;
+        issue_s(1, qb, lk(1, 0));
+        commit(&bar_empty[lk(1, 0) % NS]);
+      }
+      for (int j = 0; ok && j < nA; ++j) {
+        if (!(ok = pv(0, lk(0, j) + 1, j, tile(0, j)))) break;
+        if (alt) commit(&bar_empty[(lk(0, j) + 1) % NS]);
+        if (j + 1 < nA) {
+          if (!(ok = wait_full(lk(0, j + 1)))) break;
+          issue_s(0, qa, lk(0, j + 1));
+          if (alt) commit(&bar_empty[lk(0, j + 1) % NS]);
+        }
+        if (j < nB) {
+          if (!(ok = pv(1, lk(1, j) + 1, j, tile(1, j)))) break;
+          commit(&bar_empty[(lk(1, j) + 1) % NS]);
+          if (j + 1 < nB) {
+            if (alt && !(ok = wait_full(lk(1, j + 1)))) break;
+            issue_s(1, qb, lk(1, j + 1));
+            commit(&bar_empty[lk(1, j + 1) % NS]);
+          }
+        }
+      }
+      if (!ok) break;
+      commit(&bar_qempty[qa]);
+      if (!alt) commit(&bar_qempty[qb]);
+      qu += alt ? 1 : 2;
+      L = L0 + 2 * n;
+      ++nseg[0];
+      nseg[1] += nB > 0;
+    }
+    // every issued UMMA completes before TMEM is released
+    if (elect_one()) {
+      umma_commit(smem_u32(&bar_drain));
+      drain_wait(smem_u32(&bar_drain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int wg = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_off + wg * 128;
+    const uint32_t tOA = tmem + lane_off + C::TM_O, tOB = tmem + lane_off + C::TM_OB;
+    const uint32_t tO = wg ? tOB : tOA;
+    const float sl2 = a.scale_log2;
+    int ns = 0, no[2] = {0, 0}, nmb = 0, L = 0;  // phases so far; K/V ring loads consumed
+    bool ok = true;
+    while (ok && next_segment(a, run, per, sg)) {
+      const bool alt = sg.nb == 0;
+      const int n = sg.tiles, nA = alt ? (n + 1) / 2 : n, nB = alt ? n / 2 : n, steps = wg ? nB : nA;
+      const int L0 = L;
+      L += 2 * n;
+      const bool second = wg == 1 && !alt;                // this warpgroup works on tile B
+      const int ntok = second ? sg.nb : sg.na, tok = sg.tok + (second ? a.tpt : 0);
+      const int jt = row / a.rep, g = row - jt * a.rep;  // token in the tile, head in the group
+      const bool live = row < ntok * a.rep, busy = quarter * 32 < ntok * a.rep;  // busy: the warp has a live row
+      const int j_tok = tok + jt, gtok = sg.row0 + j_tok, head = sg.kvh * a.rep + g;
+      // the drafts this row sees, as bits (masks), or the last of them (chains)
+      unsigned long long see = 0;
+      if (a.mask != nullptr && live) {
+        const int drafts = sg.keys - sg.ctx;
+        see = a.mask[gtok] & (drafts >= 64 ? ~0ull : (1ull << drafts) - 1ull);
+      }
+      const int last_key = min(sg.ctx + j_tok, sg.keys - 1);  // chains
+      float m_run = kFloor, l_run = 0.f;
+      for (int j = 0; j < steps; ++j) {
+        const int t = sg.kt0 + (alt ? 2 * j + wg : j), key0 = t * kTile;
+        const int valid = min(sg.keys - key0, kTile);
+        ok = warp_wait(smem_u32(&bar_s[wg]), ns & 1, wc, 130);
+        if (!ok) break;
+        ++ns;
+        if ((valid & 15) != 0 && (alt || wg == 0)) {
+          // rows of V behind the last key, within its 16-key step: zero.  (After
+          // the wait for S: the slot's earlier tile has been used by then, so
+          // the wait below cannot mistake its phase.)
+          const int Lv = L0 + (alt ? 4 * j + 2 * wg : 2 * j) + 1;
+          ok = warp_wait(smem_u32(&bar_full[Lv % NS]), (Lv / NS) & 1, wc, 133);
+          if (!ok) break;
+          const int rows = 16 - (valid & 15);
+          for (int e = row; e < rows * (D / 8); e += 128) {
+            const int r = valid + e / (D / 8), c = e % (D / 8);
+            st_shared_v4(kv_addr(Lv % NS) + (c >> 3) * C::ATOM + r * 128 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!busy) {  // no live row: only the protocol
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_plo[wg]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_p[wg]));
+          ++no[wg];
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+        tmem_wait_ld();
+        if (key0 + kTile > sg.ctx) {  // drafts, or keys behind the last, in this tile
+          if (a.mask == nullptr) {
+            const int lim = last_key - key0;  // last visible column
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(neg_inf());
+          } else {
+            // visible columns as 4 words: cached keys, then the draft bits
+            const int d0 = sg.ctx - key0;  // column of draft 0 (below 0: drafts begin in an earlier tile)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int at = d0 - 32 * w;  // draft 0 relative to this word
+              uint32_t bits;
+              if (at >= 32)
+                bits = 0xffffffffu;
+              else if (at > 0)
+                bits = ((1u << at) - 1u) | static_cast<uint32_t>(see << at);
+              else
+                bits = at > -64 ? static_cast<uint32_t>(see >> -at) : 0u;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1u)) sr[w][c] = __float_as_uint(neg_inf());
+            }
+          }
+        }
+        float m4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            m4[u] = fmax3(m4[u], __uint_as_float(sr[c >> 5][(c & 31) + 2 * u]),
+                          __uint_as_float(sr[c >> 5][(c & 31) + 2 * u + 1]));
+        }
+        const float mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * sl2;
+        float alpha = 1.f;
+        bool resc = false;
+        if (j == 0) {
+          m_run = fmaxf(mx, kFloor);
+        } else if (mx > m_run + 8.f) {  // P stays below 2^8: O is rescaled rarely
+          alpha = ex2_approx(m_run - mx);
+          m_run = mx;
+          resc = true;
+        }
+        uint32_t pk[16];
+        float rs = softmax_row32(sr[0], sl2, m_run, pk);
+        tmem_st16(tS, pk);
+        rs += softmax_row32(sr[1], sl2, m_run, pk);
+        tmem_st16(tS + 16, pk);
+        if (__any_sync(0xffffffffu, resc)) {
+          // O holds P V up to the previous step once that UMMA has completed
+          ok = warp_wait(smem_u32(&bar_o[wg]), (no[wg] - 1) & 1, wc, 131);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tO + c * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_plo[wg]));
+        rs += softmax_row32(sr[2], sl2, m_run, pk);
+        tmem_st16(tS + 32, pk);
+        rs += softmax_row32(sr[3], sl2, m_run, pk);
+        tmem_st16(tS + 48, pk);
+        l_run = l_run * alpha + rs;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_p[wg]));
+        ++no[wg];
+      }
+      if (!ok) break;
+      if (wg == 0) no[1] += nB;  // warpgroup B's products, which A waits for when it joins them
+      // ---------------------------------------------------------- epilogue
+      // where the row goes: o and lse, or this CTA's part (0: the item began before, 1: it begins here)
+      float* part = a.partial + (2 * blockIdx.x + sg.first) * part_floats(D);
+      const int prow = (second ? kTile : 0) + row;
+      __nv_bfloat16* orow = a.o + (static_cast<size_t>(gtok) * a.H + head) * D;
+      auto finish = [&](float m, float l) {
+        if (!live) return;
+        if (sg.whole) {
+          a.lse[static_cast<size_t>(head) * a.T + gtok] = l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994531f;
+        } else {
+          part[2 * kTile * D + prow] = m;
+          part[2 * kTile * D + 2 * kTile + prow] = l;
+        }
+      };
+      if (steps > 0) {
+        ok = warp_wait(smem_u32(&bar_o[wg]), (no[wg] - 1) & 1, wc, 132);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (alt && wg == 1) {
+        if (steps > 0) {  // hand the row's statistics to warpgroup A, which reads O_B out of TMEM
+          b_m[row] = m_run;
+          b_l[row] = l_run;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_mb));
+        }
+      } else if (alt && nB > 0) {
+        ok = warp_wait(smem_u32(&bar_mb), nmb & 1, wc, 134) &&
+             warp_wait(smem_u32(&bar_o[1]), (no[1] - 1) & 1, wc, 135);
+        if (!ok) break;
+        ++nmb;
+        tc_fence_after();
+        const float mb = b_m[row], lb = b_l[row], m = fmaxf(m_run, mb);
+        const float fa = ex2_approx(m_run - m), fb = ex2_approx(mb - m), l = fa * l_run + fb * lb;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (busy) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t va[32], vb[32];
+            tmem_ld32(tOA + c * 32, va);
+            tmem_ld32(tOB + c * 32, vb);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              va[i] = __float_as_uint(fmaf(fa, __uint_as_float(va[i]), fb * __uint_as_float(vb[i])));
+            if (live) store_o32(orow + c * 32, part + prow * D + c * 32, sg.whole, va, inv);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bar_ofree[0]));
+          mbar_arrive(smem_u32(&bar_ofree[1]));
+        }
+        finish(m, l);
+      } else {
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        if (steps > 0) {
+          if (busy) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tO + c * 32, v);
+              tmem_wait_ld();
+              if (live) store_o32(orow + c * 32, part + prow * D + c * 32, sg.whole, v, inv);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_ofree[wg]));
+        }
+        finish(m_run, l_run);
+      }
+      if (sg.first && !sg.whole && wg == 0 && row == 0)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
+        a.desc[blockIdx.x] = make_int4(sg.ri, sg.kvh, sg.tok, sg.last_cta);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the items that more than one CTA worked on: block
+// (b, y) rows 32 y .. 32 y + 31 of the item that begins in CTA b and runs on,
+// a warp a row.  A part whose row saw no key has l = 0 and nothing in it.
+template <int D>
+__global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a) {
+  const int4 d = a.desc[blockIdx.x];
+  if (d.x < 0) return;
+  const Req r = request(a, d.x);
+  const int kvh = d.y, tok0 = d.z, first = blockIdx.x, parts = d.w - first + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int PER = D / 32;
+  const size_t stride = 2 * part_floats(D);
+  // part p of the item: slot 1 of its first CTA, slot 0 of the later ones
+  const float* base0 = a.partial + (2 * first) * part_floats(D);
+  for (int row = blockIdx.y * 32 + warp; row < blockIdx.y * 32 + 32; row += 8) {
+    const int tile = row / kTile, in = row - tile * kTile, jt = in / a.rep, tok = tok0 + tile * a.tpt + jt;
+    if (jt >= a.tpt || tok >= r.n) continue;
+    float m = kFloor;
+    for (int p = lane; p < parts; p += 32)
+      m = fmaxf(m, base0[p * stride + (p == 0) * part_floats(D) + 2 * kTile * D + row]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    float l = 0.f, acc[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const float* part = base0 + p * stride + (p == 0) * part_floats(D);
+      const float lp = part[2 * kTile * D + 2 * kTile + row];
+      const float f = ex2_approx(part[2 * kTile * D + row] - m);
+      if (lp != 0.f) {
+        l = fmaf(f, lp, l);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[k] = fmaf(f, part[row * D + lane * PER + k], acc[k]);
+      }
+    }
+    const int h = kvh * a.rep + in - jt * a.rep, tk = r.row0 + tok;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (static_cast<size_t>(tk) * a.H + h) * D + lane * PER);
+#pragma unroll
+    for (int k = 0; k < PER / 2; ++k) out[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    if (lane == 0) a.lse[static_cast<size_t>(h) * a.T + tk] = l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+template <int D>
+cudaError_t tc_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
+                      int grid, cudaStream_t stream) {
+  const cudaError_t ea =
+      cudaFuncSetAttribute(s2_cache_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::SMEM);
+  if (ea != cudaSuccess) return ea;
+  prof_before(stream, kKernelCacheAttn);
+  s2_cache_tc_kernel<D><<<grid, kThreads, TcCfg<D>::SMEM, stream>>>(tq, tk, tv, a);
+  cudaError_t e = cudaGetLastError();
+  prof_after(stream);
+  if (e != cudaSuccess) return e;
+  prof_before(stream, kKernelCacheMerge);
+  s2_cache_join_kernel<D><<<dim3(grid, 8), 256, 0, stream>>>(a);
+  e = cudaGetLastError();
+  prof_after(stream);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
+                            int D, int grid, cudaStream_t stream) {
+  return D == 64 ? tc_launch<64>(tq, tk, tv, a, grid, stream) : tc_launch<128>(tq, tk, tv, a, grid, stream);
+}
+
+}  // namespace s2

@@ -325,8 +325,9 @@ FwdSched make_fwd_sched(const Dims& d, int snake) {
 }
 
 // 4-D view {D, heads, N, B} of a bf16 [B, N, heads, D] tensor; box = one
-// box_rows x 64-column slab, 128-byte swizzle (the UMMA operand layout).
-bool make_map(CUtensorMap* m, const void* base, int B, int N, int heads, int D, int box_rows = kTile) {
+// box_rows x 64-column slab of box_heads heads, 128-byte swizzle (the UMMA operand layout).
+bool make_map(CUtensorMap* m, const void* base, int B, int N, int heads, int D, int box_rows = kTile,
+              int box_heads = 1) {
   EncodeTiledFn enc = get_encode();
   if (!enc) {
     g_last_cuda_error = -1;
@@ -336,7 +337,7 @@ bool make_map(CUtensorMap* m, const void* base, int B, int N, int heads, int D, 
                         static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(B)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(heads) * D * 2,
                            static_cast<cuuint64_t>(N) * heads * D * 2};
-  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1148,7 +1149,7 @@ int s2attn_cache_plan(const int* ctx_lens, const int* new_lens, int* block_table
 
 size_t s2attn_cache_attn_workspace_bytes(int D) {
   if (D != 64 && D != 128) return 0;
-  return static_cast<size_t>(kCacheGrid) * (sizeof(int4) + 2 * kCacheRows * (D + 2) * sizeof(float));
+  return static_cast<size_t>(kCacheTcGrid) * (sizeof(int4) + 4 * kTile * (D + 2) * sizeof(float));
 }
 
 int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_tables,
@@ -1162,6 +1163,7 @@ int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, c
     return S2ATTN_ERR_INVALID_ARG;
   if (H % Hkv != 0) return S2ATTN_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return S2ATTN_ERR_UNSUPPORTED;
+  if (H / Hkv > kTile) return S2ATTN_ERR_UNSUPPORTED;  // the heads of a kv head fill at most one row tile
   if (block_size < 16 || block_size > 256 || (block_size & (block_size - 1)) != 0) return S2ATTN_ERR_UNSUPPORTED;
   // rows, places and keys are 32-bit numbers in the kernel
   if (static_cast<int64_t>(T) * H > (1LL << 30) || static_cast<int64_t>(num_blocks) * block_size > 0x7fffffffLL ||
@@ -1198,6 +1200,18 @@ int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, c
   a.max_blocks = max_blocks;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(D)));
   if (!status_block(&a.status)) return S2ATTN_ERR_CUDA;
+  a.wait_limit_ns = wait_limit_ns();
+  a.tpt = kTile / a.rep;
+  if (override_value(tile_override(), "cache") != "mma") {
+    const int rows = block_size < kTile ? block_size : kTile;
+    CUtensorMap tq, tk, tv;
+    if (!make_map(&tq, q, 1, T, H, D, a.tpt, a.rep) || !make_map(&tk, k_cache, 1, num_blocks * block_size, Hkv, D, rows) ||
+        !make_map(&tv, v_cache, 1, num_blocks * block_size, Hkv, D, rows))
+      return S2ATTN_ERR_CUDA;
+    a.partial = reinterpret_cast<float*>(a.desc + kCacheTcGrid);
+    const int grid = info.sms < kCacheTcGrid ? info.sms : kCacheTcGrid;
+    return launched(launch_cache_tc(tq, tk, tv, a, D, grid, static_cast<cudaStream_t>(stream)), 2);
+  }
   const int grid = 2 * info.sms < kCacheGrid ? 2 * info.sms : kCacheGrid;
   return launched(launch_cache_attn(a, D, grid, static_cast<cudaStream_t>(stream)), 2);
 }
