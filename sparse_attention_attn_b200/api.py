@@ -24,6 +24,12 @@ def _stream(device=None) -> int:
 
 
 def _need(name: str, t: torch.Tensor, shape, dtype=torch.bfloat16, device=None) -> None:
+    try:  # the usual case in as few steps as it takes; what fails is named below
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            if t.is_cuda if device is None else t.device == device:
+                return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -462,6 +468,19 @@ def nf4_dequantize(codes, scale_codes, c2, out=None):
     return out
 
 
+def _run(dev, fn: str, *args) -> None:
+    """One C call with `dev` current, on its current stream.  The device guard
+    is entered only where it changes something: the smallest calls take a few
+    microseconds on the GPU, and the guard as long on the host."""
+    if torch.cuda.current_device() == dev.index:
+        st = getattr(_lib.load(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(_lib.load(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != _lib.S2ATTN_OK:
+        _lib._check(fn, st)
+
+
 # ---------------------------------------------------------------- query/key norm with rotation
 
 def _need_norm_weights(w_q, w_k, D: int, dev) -> int:
@@ -492,15 +511,10 @@ def qknorm_rope_forward(q, k, w_q, w_k, table, eps: float = 1e-6, q_out=None, k_
     _need("k", k, (B, N, Hkv, D), device=dev)
     w32 = _need_norm_weights(w_q, w_k, D, dev)
     _need_table(table, D, dev, N)
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k_out is None else k_out
-    _need("q_out", q_out, (B, N, H, D), device=dev)
-    _need("k_out", k_out, (B, N, Hkv, D), device=dev)
-    with torch.cuda.device(dev):
-        st = _lib.s2attn_qknorm_rope_fwd(q.data_ptr(), k.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), table.data_ptr(),
-                                         q_out.data_ptr(), k_out.data_ptr(), B, N, H, Hkv, D, w32, float(eps),
-                                         _stream(dev))
-    _lib._check("s2attn_qknorm_rope_fwd", st)
+    q_out = _out("q_out", q_out, q)
+    k_out = _out("k_out", k_out, k)
+    _run(dev, "s2attn_qknorm_rope_fwd", q.data_ptr(), k.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), table.data_ptr(),
+         q_out.data_ptr(), k_out.data_ptr(), B, N, H, Hkv, D, w32, float(eps))
     return q_out, k_out
 
 
@@ -517,23 +531,22 @@ def qknorm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, table, eps: float = 1e-
     _need("dk_out", dk_out, (B, N, Hkv, D), device=dev)
     w32 = _need_norm_weights(w_q, w_k, D, dev)
     _need_table(table, D, dev, N)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dw_q = torch.empty_like(w_q) if dw_q is None else dw_q
-    dw_k = torch.empty_like(w_k) if dw_k is None else dw_k
-    _need("dq", dq, (B, N, H, D), device=dev)
-    _need("dk", dk, (B, N, Hkv, D), device=dev)
-    _need("dw_q", dw_q, (D,), w_q.dtype, device=dev)
-    _need("dw_k", dw_k, (D,), w_q.dtype, device=dev)
+    dq, dk = _out("dq", dq, q), _out("dk", dk, k)
+    dw_q, dw_k = _out("dw_q", dw_q, w_q), _out("dw_k", dw_k, w_k)
     workspace, wsb = _workspace("s2attn_qknorm_rope_bwd", workspace, _lib.s2attn_qknorm_rope_bwd_workspace_bytes(D),
                                 dev)
-    with torch.cuda.device(dev):
-        st = _lib.s2attn_qknorm_rope_bwd(q.data_ptr(), k.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), table.data_ptr(),
-                                         dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                         dw_q.data_ptr(), dw_k.data_ptr(), B, N, H, Hkv, D, w32, float(eps),
-                                         workspace.data_ptr(), wsb, _stream(dev))
-    _lib._check("s2attn_qknorm_rope_bwd", st)
+    _run(dev, "s2attn_qknorm_rope_bwd", q.data_ptr(), k.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), table.data_ptr(),
+         dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dw_q.data_ptr(), dw_k.data_ptr(), B, N,
+         H, Hkv, D, w32, float(eps), workspace.data_ptr(), wsb)
     return dq, dk, dw_q, dw_k
+
+
+def _out(name: str, t, like):
+    """The caller's output checked against the tensor it is shaped like, or a new one."""
+    if t is None:
+        return torch.empty_like(like)
+    _need(name, t, like.shape, like.dtype, device=like.device)
+    return t
 
 
 def _workspace(fn: str, workspace, need: int, dev):
@@ -620,13 +633,10 @@ def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, n
     buf = torch.empty(2 * T + R + 5, dtype=torch.int32, device=dev)  # one allocation
     positions, slots, cu_seqlens, counts = buf.split((T, T, R + 1, 4))
     p = buf.data_ptr()
-    with torch.cuda.device(dev):
-        st = _lib.s2attn_cache_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
-                                    free_blocks.data_ptr(), None if parents is None else parents.data_ptr(),
-                                    p + 8 * T, p, p + 4 * T, None if mask is None else mask.data_ptr(),
-                                    p + 4 * (2 * T + R + 1), R, block_tables.shape[1], free_blocks.shape[0],
-                                    int(block_size), T, _stream(dev))
-    _lib._check("s2attn_cache_plan", st)
+    _run(dev, "s2attn_cache_plan", ctx_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
+         free_blocks.data_ptr(), None if parents is None else parents.data_ptr(), p + 8 * T, p, p + 4 * T, None if
+         mask is None else mask.data_ptr(), p + 4 * (2 * T + R + 1), R, block_tables.shape[1], free_blocks.shape[0],
+         int(block_size), T)
     return CachePlan(cu_seqlens, positions, slots, mask, counts)
 
 
@@ -665,15 +675,11 @@ def cache_append(q, k, v, table, positions, slots, k_cache, v_cache, w_q=None, w
     if (w_q is None) != (w_k is None):
         raise ValueError("w_q and w_k go together")
     w32 = 0 if w_q is None else _need_norm_weights(w_q, w_k, D, dev)
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    _need("q_out", q_out, (T, H, D), device=dev)
-    with torch.cuda.device(dev):
-        st = _lib.s2attn_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                      None if w_q is None else w_q.data_ptr(),
-                                      None if w_k is None else w_k.data_ptr(), table.data_ptr(),
-                                      positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
-                                      v_cache.data_ptr(), T, H, Hkv, D, rows, nb * bs, w32, float(eps), _stream(dev))
-    _lib._check("s2attn_cache_append", st)
+    q_out = _out("q_out", q_out, q)
+    _run(dev, "s2attn_cache_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), None if w_q is None else
+         w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), table.data_ptr(), positions.data_ptr(),
+         slots.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, H, Hkv, D, rows, nb * bs, w32,
+         float(eps))
     return q_out
 
 
@@ -701,15 +707,13 @@ def cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mas
     _need_ints("cu_seqlens", cu_seqlens, (R + 1,), dev)
     if mask is not None:
         _need("mask", mask, (T,), torch.int64, device=dev)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((H, T), dtype=torch.float32, device=dev) if lse is None else lse
-    _need("out", out, (T, H, D), device=dev)
-    _need("lse", lse, (H, T), torch.float32, device=dev)
+    out = _out("out", out, q)
+    if lse is None:
+        lse = torch.empty((H, T), dtype=torch.float32, device=dev)
+    else:
+        _need("lse", lse, (H, T), torch.float32, device=dev)
     workspace, wsb = _workspace("s2attn_cache_attn", workspace, _lib.s2attn_cache_attn_workspace_bytes(D), dev)
-    with torch.cuda.device(dev):
-        st = _lib.s2attn_cache_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                                    ctx_lens.data_ptr(), cu_seqlens.data_ptr(),
-                                    None if mask is None else mask.data_ptr(), out.data_ptr(), lse.data_ptr(), T, R,
-                                    H, Hkv, D, nb, bs, maxb, workspace.data_ptr(), wsb, _stream(dev))
-    _lib._check("s2attn_cache_attn", st)
+    _run(dev, "s2attn_cache_attn", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+         ctx_lens.data_ptr(), cu_seqlens.data_ptr(), None if mask is None else mask.data_ptr(), out.data_ptr(),
+         lse.data_ptr(), T, R, H, Hkv, D, nb, bs, maxb, workspace.data_ptr(), wsb)
     return out, lse

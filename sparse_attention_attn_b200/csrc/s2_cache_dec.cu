@@ -1,0 +1,390 @@
+// Attention of few new tokens over a paged cache: decoding, and short chains or
+// trees of drafts (at most 16 rows of (token, head) share a kv head's keys in a
+// tile).  The same operation as s2_cache_tc.cu, for calls that reading the
+// cache bounds: with one row in 16 or 4 in 128 the tensor work is small
+// whatever unit does it, and what counts is that loads never stop.
+//
+// Rows.  The rep = H/Hkv <= 16 query heads of a kv head form one 16-row tile
+// with floor(16 / rep) tokens: row = token * rep + head in group, the order a
+// {64 columns, rep heads, tokens} TMA box lands in shared memory.
+//
+// Two CTAs an SM, each a TMA producer warp and four consumer warps.  The
+// producer walks the CTA's segments on its own, through a ring of 64-key stages
+// (K and V, 32 KB at head dim 128: 6 stages an SM, 192 KB in flight where some
+// 45 KB cover the latency at full bandwidth), and hands each segment's
+// description and query rows over in a two-slot ring, so that no load waits for
+// arithmetic and the stages keep filling across segments.  A consumer warp
+// takes 16 of a stage's 64 keys through mma.sync with its own running maximum
+// and sum (fp32): no synchronisation inside a segment but the stages' own
+// barriers.  At its end the four warps join through the last stage's memory.
+// P is rounded to bf16 for the product with V, its sums are taken before.
+//
+// Rows of V behind the last key may hold anything (stale cache rows): the
+// fragments that hold them are zeroed in registers.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "s2_cache.cuh"
+
+namespace s2 {
+
+namespace {
+
+using namespace cache;
+
+constexpr int kRows = kCacheRows;  // rows of a tile
+constexpr int kKeys = 64;          // keys of a stage
+constexpr int kWarps = 4;          // consumers
+constexpr int kDecThreads = 32 * (kWarps + 1);
+
+template <int D>
+struct DecCfg {
+  static constexpr int NS = D == 128 ? 3 : 6;       // stages
+  static constexpr int SLAB = kKeys * 128;          // one 64-column slab of a stage's K or V
+  static constexpr int TILE = kKeys * D * 2;        // K or V
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int QSLAB = kRows * 128;
+  static constexpr int QSLOT = kRows * D * 2;
+  static constexpr int OFF_Q = NS * STAGE;
+  static constexpr int SMEM = OFF_Q + 2 * QSLOT + 1024;
+  static constexpr int JROW = D + 4;                // floats of a row in the join
+  static_assert(2 * kRows * JROW * 4 + 4 * kRows * 4 <= STAGE, "the join fits a stage");
+  static_assert(2 * (SMEM + 2048) <= 233472, "two CTAs an SM");
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Barrier of the consumer warps alone.
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+
+// Address of 16-byte chunk c of row r in slabs of `slab` bytes written by TMA
+// with the 128-byte swizzle (slabs 1024-byte aligned).
+__device__ __forceinline__ uint32_t swz(uint32_t base, int slab, int r, int c) {
+  return base + (c >> 3) * slab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads, 2)
+    s2_cache_dec_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a) {
+  using C = DecCfg<D>;
+  constexpr int NS = C::NS;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_qfull[2], bar_qempty[2];
+  __shared__ uint32_t abort_flag;
+  __shared__ long long sums[kDecThreads / 32], found[2];
+  __shared__ Seg segs[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  launch_dependents();
+  if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  Run run;
+  if (!locate<kDecThreads, kKeys>(a, a.tpt, kCacheMinUnits, sums, found, run)) return;
+  const uint32_t sbase = smem_u32(smem);
+  WaitCtx wc{&abort_flag, a.status, a.wait_limit_ns};
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), kWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bar_qfull[s]), 1);
+      mbar_init(smem_u32(&bar_qempty[s]), kWarps);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    int L = 0, qu = 0;
+    bool ok = true;
+    const int page_log2 = min(a.bs_log2, 6), page_rows = 1 << page_log2;
+    Seg sg;
+    for (;;) {
+      const bool more = next_segment<kKeys>(a, a.tpt, run, sg);
+      const int qs = qu & 1;
+      if (qu > 1 && !(ok = warp_wait(smem_u32(&bar_qempty[qs]), ((qu >> 1) - 1) & 1, wc, 140))) break;
+      if (lane == 0) {
+        if (!more) sg.tiles = -1;
+        segs[qs] = sg;
+        if (more && sg.tiles > 0) {
+          mbar_arrive_expect_tx(smem_u32(&bar_qfull[qs]), a.tpt * a.rep * 128 * (D / 64));
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sbase + C::OFF_Q + qs * C::QSLOT + c * C::QSLAB, &tmQ, smem_u32(&bar_qfull[qs]), c * 64,
+                        sg.kvh * a.rep, sg.row0 + sg.tok, 0);
+        } else {
+          mbar_arrive(smem_u32(&bar_qfull[qs]));
+        }
+      }
+      __syncwarp();
+      ++qu;
+      if (!more) break;
+      const int* table = a.block_tables + static_cast<size_t>(sg.ri) * a.max_blocks;
+      for (int i = 0; ok && i < sg.tiles; ++i) {
+        const int key = (sg.kt0 + i) * kKeys + (lane << page_log2);
+        const bool mine = lane < (kKeys >> page_log2) && key < sg.keys;
+        int row = 0;  // a block outside the cache reads as zeros: its row lies behind the tensor
+        if (mine) {
+          const int blk = table[key >> a.bs_log2];
+          row = data_in_range(a.status, blk, a.num_blocks, 711) ? (blk << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))
+                                                                : a.num_blocks << a.bs_log2;
+        }
+        const int s = L % NS, r = L / NS, pages = __popc(__ballot_sync(0xffffffffu, mine));
+        if (r > 0 && !(ok = warp_wait(smem_u32(&bar_empty[s]), (r - 1) & 1, wc, 141))) break;
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bar_full[s]), 2 * pages * page_rows * 128 * (D / 64));
+        __syncwarp();
+        if (mine)
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t dst = sbase + s * C::STAGE + c * C::SLAB + (lane << page_log2) * 128;
+            tma_load_4d(dst, &tmK, smem_u32(&bar_full[s]), c * 64, sg.kvh, row, 0);
+            tma_load_4d(dst + C::TILE, &tmV, smem_u32(&bar_full[s]), c * 64, sg.kvh, row, 0);
+          }
+        __syncwarp();
+        ++L;
+      }
+      if (!ok) break;
+    }
+    if (*wc.abort && lane == 0) {
+      // never leave copies in flight into shared memory: wait (bounded) for
+      // the last fill of every slot
+      for (int s = 0; s < 2 && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / 2) & 1);
+      for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
+    }
+  } else {
+    // ------------------------------------------------------------ consumers
+    const float sl2 = a.scale_log2;
+    int L = 0;
+    for (int qu = 0;; ++qu) {
+      const int qs = qu & 1;
+      if (!warp_wait(smem_u32(&bar_qfull[qs]), (qu >> 1) & 1, wc, 142)) break;
+      const Seg sg = segs[qs];
+      if (sg.tiles < 0) break;
+      // ---- Q fragments (rows lane / 4 and lane / 4 + 8), and the slot back
+      uint32_t qf[D / 16][4];
+      if (sg.tiles > 0) {
+        const uint32_t sq = sbase + C::OFF_Q + qs * C::QSLOT;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) ldsm4(qf[k], swz(sq, C::QSLAB, lane & 15, 2 * k + (lane >> 4)));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_qempty[qs]));
+      const int rows = sg.ntok * a.rep;
+      int last_key[2];  // chains: the last key of the lane's two rows
+      unsigned long long see[2] = {0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = (lane >> 2) + 8 * h, j = row < rows ? sg.tok + row / a.rep : sg.tok;
+        last_key[h] = min(sg.ctx + j, sg.keys - 1);
+        if (a.mask != nullptr) see[h] = visible_drafts(a, sg, sg.row0 + j);
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+      float m[2] = {kFloor, kFloor}, l[2] = {0.f, 0.f};
+      bool ok = true;
+      for (int i = 0; i < sg.tiles; ++i, ++L) {
+        const int s = L % NS;
+        if (!(ok = warp_wait(smem_u32(&bar_full[s]), (L / NS) & 1, wc, 143))) break;
+        const uint32_t sk = sbase + s * C::STAGE, sv = sk + C::TILE;
+        const int key0 = (sg.kt0 + i) * kKeys + warp * 16;
+        if (key0 < sg.keys) {
+          // S = Q K^T for this warp's 16 keys: two n-tiles of 8
+          float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          const int krow = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];
+            ldsm4(b, swz(sk, C::SLAB, krow, 2 * k + ((lane >> 3) & 1)));
+            mma16816(sc[0], qf[k], b[0], b[1]);
+            mma16816(sc[1], qf[k], b[2], b[3]);
+          }
+          if (key0 + 16 > sg.ctx) {  // some key of the warp is a draft or behind the last
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + n * 8 + (lane & 3) * 2 + (e & 1), h = e >> 1, d = key - sg.ctx;
+                const bool vis = a.mask == nullptr ? key <= last_key[h] : d < 0 || (d < 64 && (see[h] >> (d & 63) & 1));
+                if (!vis) sc[n][e] = neg_inf();
+              }
+          }
+          uint32_t pf[4];
+          float alpha[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float mx = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[h], mx * sl2);
+            alpha[h] = ex2_approx(m[h] - mn);
+            m[h] = mn;
+            const float p0 = ex2_approx(fmaf(sc[0][2 * h], sl2, -mn)), p1 = ex2_approx(fmaf(sc[0][2 * h + 1], sl2, -mn));
+            const float p2 = ex2_approx(fmaf(sc[1][2 * h], sl2, -mn)), p3 = ex2_approx(fmaf(sc[1][2 * h + 1], sl2, -mn));
+            l[h] = l[h] * alpha[h] + ((p0 + p1) + (p2 + p3));
+            pf[h] = pack_bf16x2(p0, p1);
+            pf[h + 2] = pack_bf16x2(p2, p3);
+          }
+          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+              o[d][0] *= alpha[0];
+              o[d][1] *= alpha[0];
+              o[d][2] *= alpha[1];
+              o[d][3] *= alpha[1];
+            }
+          }
+          // V's rows behind the last key: this lane's fragments hold keys key0 + (lane & 3) 2 (+1) (+8)
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+          const bool ragged = key0 + 16 > sg.keys;
+          if (ragged) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int key = key0 + (lane & 3) * 2 + 8 * x;
+              keep[x] = (key < sg.keys ? 0xffffu : 0u) | (key + 1 < sg.keys ? 0xffff0000u : 0u);
+            }
+          }
+          const int vrow = warp * 16 + (lane & 15);
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            uint32_t b[4];
+            ldsm4t(b, swz(sv, C::SLAB, vrow, 2 * d + (lane >> 4)));
+            if (ragged) {
+              b[0] &= keep[0];
+              b[1] &= keep[1];
+              b[2] &= keep[0];
+              b[3] &= keep[1];
+            }
+            mma16816(o[2 * d], pf, b[0], b[1]);
+            mma16816(o[2 * d + 1], pf, b[2], b[3]);
+          }
+        }
+        __syncwarp();
+        if (i + 1 < sg.tiles && lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));  // the last stage serves the join first
+      }
+      if (!ok) break;
+      // ---- join the warps: 2 and 3 into 0 and 1, then 1 into 0, a row per lane quad
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      }
+      if (sg.tiles > 0) {
+        const int s = (L - 1) % NS;
+        float* jo = reinterpret_cast<float*>(smem + s * C::STAGE);  // [2][row][D + 4]
+        float* jm = jo + 2 * kRows * C::JROW;                       // [2][row] maxima, then sums
+#pragma unroll
+        for (int half = 2; half > 0; half >>= 1) {
+          consumer_sync();  // the stage (or the buffers of the step before) have been read
+          if (warp >= half && warp < 2 * half) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = (lane >> 2) + 8 * h, at = (warp - half) * kRows + row;
+              if (8 * h < rows) {
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d)
+                  *reinterpret_cast<float2*>(jo + at * C::JROW + d * 8 + (lane & 3) * 2) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
+                if ((lane & 3) == 0) {
+                  jm[at] = m[h];
+                  jm[2 * kRows + at] = l[h];
+                }
+              }
+            }
+          }
+          consumer_sync();
+          if (warp < half) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = (lane >> 2) + 8 * h, at = warp * kRows + row;
+              if (8 * h < rows) {
+                const float om = jm[at], mn = fmaxf(m[h], om), fa = ex2_approx(m[h] - mn), fb = ex2_approx(om - mn);
+                m[h] = mn;
+                l[h] = fa * l[h] + fb * jm[2 * kRows + at];
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                  const float2 v = *reinterpret_cast<const float2*>(jo + at * C::JROW + d * 8 + (lane & 3) * 2);
+                  o[d][2 * h] = fmaf(fa, o[d][2 * h], fb * v.x);
+                  o[d][2 * h + 1] = fmaf(fa, o[d][2 * h + 1], fb * v.y);
+                }
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();  // these accesses before the TMA that refills the stage
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));
+      }
+      // ---- out: o and lse, or this CTA's part (slot 0: the item began before, 1: it begins here)
+      if (warp == 0) {
+        float* part = Part<kRows, D>::at(a, blockIdx.x, sg.first);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = (lane >> 2) + 8 * h;
+          if (row >= rows) continue;
+          if (sg.whole) {
+            const int jt = row / a.rep, head = sg.kvh * a.rep + row - jt * a.rep, tk = sg.row0 + sg.tok + jt;
+            const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+            __nv_bfloat16* dst = a.o + (static_cast<size_t>(tk) * a.H + head) * D + (lane & 3) * 2;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d)
+              *reinterpret_cast<uint32_t*>(dst + d * 8) = pack_bf16x2(o[d][2 * h] * inv, o[d][2 * h + 1] * inv);
+            if ((lane & 3) == 0) a.lse[static_cast<size_t>(head) * a.T + tk] = lse_of(m[h], l[h]);
+          } else {
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d)
+              *reinterpret_cast<float2*>(part + row * D + d * 8 + (lane & 3) * 2) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
+            if ((lane & 3) == 0) {
+              part[kRows * D + row] = m[h];
+              part[kRows * (D + 1) + row] = l[h];
+            }
+          }
+        }
+        if (lane == 0 && sg.first && !sg.whole)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
+          a.desc[blockIdx.x] = make_int4(sg.ri, sg.kvh, sg.tok, sg.last_cta);
+      }
+    }
+  }
+}
+
+template <int D>
+cudaError_t dec_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
+                       int grid, cudaStream_t stream) {
+  const cudaError_t ea =
+      cudaFuncSetAttribute(s2_cache_dec_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<D>::SMEM);
+  if (ea != cudaSuccess) return ea;
+  prof_before(stream, kKernelCacheAttn);
+  s2_cache_dec_kernel<D><<<grid, kDecThreads, DecCfg<D>::SMEM, stream>>>(tq, tk, tv, a);
+  const cudaError_t e = cudaGetLastError();
+  prof_after(stream);
+  if (e != cudaSuccess) return e;
+  return launch_join<kRows, kRows, kKeys, D>(a, a.tpt, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_dec(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
+                             int D, int grid, cudaStream_t stream) {
+  return D == 64 ? dec_launch<64>(tq, tk, tv, a, grid, stream) : dec_launch<128>(tq, tk, tv, a, grid, stream);
+}
+
+}  // namespace s2

@@ -14,13 +14,7 @@
 // order a {64 columns, rep heads, tokens} TMA box lands in shared memory.  An
 // item is two adjacent tiles (A, B) of one (request, kv head).
 //
-// Split.  A unit is 128 keys of one item; all units of a batch are numbered
-// request by request and dealt to the CTAs (one per SM) in equal contiguous
-// runs, so that a batch of very different lengths, or one long request, loads
-// every SM alike.  A run that covers only part of an item's keys (a segment)
-// leaves unnormalised sums, row maxima and row sums in the workspace, and a
-// second kernel joins the parts in order: the split depends on the lengths
-// alone, so the same call gives the same bits.
+// Split.  One CTA per SM walks an equal run of units of 128 keys (s2_cache.cuh).
 //
 // Two ways through a segment keep both softmax warpgroups and the tensor core
 // busy.  Paired (the item has tile B): every key tile feeds both query tiles,
@@ -44,15 +38,16 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "s2_common.cuh"
-#include "s2_ptx.cuh"
+#include "s2_cache.cuh"
 
 namespace s2 {
 
 namespace {
 
+using namespace cache;
+
 constexpr int kThreads = 320;
-constexpr float kFloor = -3.0e38f;  // running maximum of a row that has seen no key (finite: no inf - inf)
+constexpr int kPair = 2 * kTile;  // rows of an item
 
 template <int D>
 struct TcCfg {
@@ -65,89 +60,6 @@ struct TcCfg {
   static constexpr uint32_t TM_O = 256, TM_OB = 384;
   static_assert(SMEM <= 232448 - 2048, "shared memory");
 };
-
-// The lengths of request i, and its units.
-struct Req {
-  int ctx, n, row0;  // cached tokens, new tokens, first row of q
-  int keys;          // keys in all
-  int kt, np;        // key tiles, items a kv head
-  long long units;   // Hkv * np * kt
-};
-__device__ __forceinline__ Req request(const CacheAttnArgs& a, int i) {
-  Req r;
-  r.row0 = min(max(a.cu_seqlens[i], 0), a.T);
-  const int end = min(max(a.cu_seqlens[i + 1], r.row0), a.T);
-  r.n = end - r.row0;
-  const long long most = static_cast<long long>(a.max_blocks) << a.bs_log2;  // places the table has
-  r.ctx = static_cast<int>(min(static_cast<long long>(max(a.ctx_lens[i], 0)), most));
-  r.keys = static_cast<int>(min(static_cast<long long>(r.ctx) + r.n, most));
-  r.kt = (r.keys + kTile - 1) / kTile;
-  r.np = (r.n + 2 * a.tpt - 1) / (2 * a.tpt);
-  r.units = static_cast<long long>(a.Hkv) * r.np * r.kt;
-  return r;
-}
-
-// A CTA's run of units and the walk through its segments.
-struct Run {
-  long long u0, u1, rbase;  // units of the run; first unit of request ri
-  int ri;
-};
-struct Seg {
-  int ri, kvh;
-  int row0, n, ctx, keys;  // the request (row0: first row of q)
-  int tok;                 // first token of tile A in the request
-  int na, nb;              // tokens of tiles A and B (nb = 0: alternating)
-  int kt0, tiles;          // first key tile, key tiles to work on (0: none is visible)
-  int whole, first;        // the whole item; the part with key tile 0
-  int last_cta;            // first && !whole: CTA with the item's last part
-};
-__device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, Run& w, long long per, Seg& s) {
-  while (w.u0 < w.u1) {
-    const Req r = request(a, w.ri);
-    if (w.u0 >= w.rbase + r.units) {
-      w.rbase += r.units;
-      ++w.ri;
-      continue;
-    }
-    const long long in = w.u0 - w.rbase, item = in / r.kt;  // item = kvh * np + pair
-    const int pair = static_cast<int>(item % r.np);
-    s.ri = w.ri;
-    s.kvh = static_cast<int>(item / r.np);
-    s.row0 = r.row0;
-    s.n = r.n;
-    s.ctx = r.ctx;
-    s.keys = r.keys;
-    s.tok = pair * 2 * a.tpt;
-    s.na = min(a.tpt, r.n - s.tok);
-    s.nb = min(a.tpt, r.n - s.tok - s.na);
-    s.kt0 = static_cast<int>(in - item * r.kt);
-    const int kt1 = static_cast<int>(min(static_cast<long long>(r.kt), s.kt0 + (w.u1 - w.u0)));
-    // chains: keys behind the item's last token are not visited
-    const int reach = a.mask != nullptr ? r.keys : min(r.ctx + min(s.tok + s.na + s.nb, r.keys - r.ctx), r.keys);
-    s.tiles = max(min(kt1, (reach + kTile - 1) / kTile) - s.kt0, 0);
-    s.first = s.kt0 == 0;
-    s.whole = s.first && kt1 == r.kt;
-    s.last_cta = static_cast<int>((w.rbase + (item + 1) * r.kt - 1) / per);
-    w.u0 += kt1 - s.kt0;
-    return true;
-  }
-  return false;
-}
-
-// Sum of v over the block; every thread gets it.
-__device__ __forceinline__ long long block_sum(long long v, long long* buf) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) v += buf[w];
-  return v;
-}
-
-__device__ __forceinline__ size_t part_floats(int D) { return static_cast<size_t>(2 * kTile) * (D + 2); }
 
 // acc (bit patterns, 32 columns from c0 of one row) out: o normalised, or the partial as it is.
 __device__ __forceinline__ void store_o32(__nv_bfloat16* o, float* part, bool whole, const uint32_t (&v)[32], float inv) {
@@ -172,49 +84,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_qfull[NQ], bar_qempty[NQ], bar_full[NS], bar_empty[NS], bar_s[2], bar_plo[2],
       bar_p[2], bar_o[2], bar_ofree[2], bar_mb, bar_drain;
   __shared__ uint32_t tmem_slot, abort_flag;
-  __shared__ long long sums[kThreads / 32], found_before;
-  __shared__ int found;
+  __shared__ long long sums[kThreads / 32], found[2];
   __shared__ float b_m[kTile], b_l[kTile];  // alternating: warpgroup B's row maxima and sums
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // ---- the run of units of this CTA and the request it begins in
-  long long total = 0;
-  for (int base = 0; base < a.R; base += kThreads) {
-    const int i = base + tid;
-    total += block_sum(i < a.R ? request(a, i).units : 0, sums);
-  }
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, 1LL);
-  Run run;
-  run.u0 = per * blockIdx.x;
-  run.u1 = min(run.u0 + per, total);
+  launch_dependents();
   if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (run.u0 >= run.u1) return;
-  long long before = 0;
-  for (int base = 0; base < a.R; base += kThreads) {
-    const int i = base + tid;
-    const long long mine = i < a.R ? request(a, i).units : 0;
-    long long inc = mine;  // inclusive scan of the chunk
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, m);
-      if (lane >= m) inc += o;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    long long all = 0, mybase = before;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) mybase += sums[w];
-      all += sums[w];
-    }
-    if (run.u0 >= mybase + inc - mine && run.u0 < mybase + inc) {
-      found = i;
-      found_before = mybase + inc - mine;
-    }
-    before += all;
-    if (run.u0 < before) break;  // uniform
-  }
+  Run run;
+  if (!locate<kThreads, kTile>(a, 2 * a.tpt, 1, sums, found, run)) return;
   WaitCtx wc{&abort_flag, a.status, a.wait_limit_ns};
   const uint32_t sQ = smem_u32(smem);
   auto q_addr = [&](int s) { return sQ + s * C::TILE; };
@@ -248,9 +125,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  run.ri = found;
-  run.rbase = found_before;
   Seg sg;
+  // the next segment; tiles A and B of its item have na and nb tokens (nb = 0: alternating)
+  int na, nb;
+  auto next = [&]() {
+    if (!next_segment<kTile>(a, 2 * a.tpt, run, sg)) return false;
+    na = min(sg.ntok, a.tpt);
+    nb = sg.ntok - na;
+    return true;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -290,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++L;
       return true;
     };
-    while (ok && next_segment(a, run, per, sg)) {
+    while (ok && next()) {
       if (sg.tiles == 0) continue;
-      ok = load_q(sg.row0 + sg.tok) && (sg.nb == 0 || load_q(sg.row0 + sg.tok + a.tpt));
+      ok = load_q(sg.row0 + sg.tok) && (nb == 0 || load_q(sg.row0 + sg.tok + a.tpt));
       const int* table = a.block_tables + static_cast<size_t>(sg.ri) * a.max_blocks;
       for (int i = 0; ok && i < sg.tiles; ++i) {
         const int key = (sg.kt0 + i) * kTile + (lane << page_log2);
@@ -363,9 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     bool ok = true;
-    while (ok && next_segment(a, run, per, sg)) {
+    while (ok && next()) {
       if (sg.tiles == 0) continue;
-      const bool alt = sg.nb == 0;
+      const bool alt = nb == 0;
       const int n = sg.tiles, nA = alt ? (n + 1) / 2 : n, nB = alt ? n / 2 : n;
       const int qa = qu % NQ, qb = alt ? qa : (qu + 1) % NQ, L0 = L;
       // load of the K tile of step j (its V tile is the next load), and the key tile
@@ -423,22 +306,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     int ns = 0, no[2] = {0, 0}, nmb = 0, L = 0;  // phases so far; K/V ring loads consumed
     bool ok = true;
-    while (ok && next_segment(a, run, per, sg)) {
-      const bool alt = sg.nb == 0;
+    while (ok && next()) {
+      const bool alt = nb == 0;
       const int n = sg.tiles, nA = alt ? (n + 1) / 2 : n, nB = alt ? n / 2 : n, steps = wg ? nB : nA;
       const int L0 = L;
       L += 2 * n;
       const bool second = wg == 1 && !alt;                // this warpgroup works on tile B
-      const int ntok = second ? sg.nb : sg.na, tok = sg.tok + (second ? a.tpt : 0);
+      const int ntok = second ? nb : na, tok = sg.tok + (second ? a.tpt : 0);
       const int jt = row / a.rep, g = row - jt * a.rep;  // token in the tile, head in the group
       const bool live = row < ntok * a.rep, busy = quarter * 32 < ntok * a.rep;  // busy: the warp has a live row
       const int j_tok = tok + jt, gtok = sg.row0 + j_tok, head = sg.kvh * a.rep + g;
       // the drafts this row sees, as bits (masks), or the last of them (chains)
       unsigned long long see = 0;
-      if (a.mask != nullptr && live) {
-        const int drafts = sg.keys - sg.ctx;
-        see = a.mask[gtok] & (drafts >= 64 ? ~0ull : (1ull << drafts) - 1ull);
-      }
+      if (a.mask != nullptr && live) see = visible_drafts(a, sg, gtok);
       const int last_key = min(sg.ctx + j_tok, sg.keys - 1);  // chains
       float m_run = kFloor, l_run = 0.f;
       for (int j = 0; j < steps; ++j) {
@@ -556,16 +436,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wg == 0) no[1] += nB;  // warpgroup B's products, which A waits for when it joins them
       // ---------------------------------------------------------- epilogue
       // where the row goes: o and lse, or this CTA's part (0: the item began before, 1: it begins here)
-      float* part = a.partial + (2 * blockIdx.x + sg.first) * part_floats(D);
+      float* part = Part<kPair, D>::at(a, blockIdx.x, sg.first);
       const int prow = (second ? kTile : 0) + row;
       __nv_bfloat16* orow = a.o + (static_cast<size_t>(gtok) * a.H + head) * D;
       auto finish = [&](float m, float l) {
         if (!live) return;
         if (sg.whole) {
-          a.lse[static_cast<size_t>(head) * a.T + gtok] = l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994531f;
+          a.lse[static_cast<size_t>(head) * a.T + gtok] = lse_of(m, l);
         } else {
-          part[2 * kTile * D + prow] = m;
-          part[2 * kTile * D + 2 * kTile + prow] = l;
+          part[kPair * D + prow] = m;
+          part[kPair * (D + 1) + prow] = l;
         }
       };
       if (steps > 0) {
@@ -640,51 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the items that more than one CTA worked on: block
-// (b, y) rows 32 y .. 32 y + 31 of the item that begins in CTA b and runs on,
-// a warp a row.  A part whose row saw no key has l = 0 and nothing in it.
-template <int D>
-__global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a) {
-  const int4 d = a.desc[blockIdx.x];
-  if (d.x < 0) return;
-  const Req r = request(a, d.x);
-  const int kvh = d.y, tok0 = d.z, first = blockIdx.x, parts = d.w - first + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int PER = D / 32;
-  const size_t stride = 2 * part_floats(D);
-  // part p of the item: slot 1 of its first CTA, slot 0 of the later ones
-  const float* base0 = a.partial + (2 * first) * part_floats(D);
-  for (int row = blockIdx.y * 32 + warp; row < blockIdx.y * 32 + 32; row += 8) {
-    const int tile = row / kTile, in = row - tile * kTile, jt = in / a.rep, tok = tok0 + tile * a.tpt + jt;
-    if (jt >= a.tpt || tok >= r.n) continue;
-    float m = kFloor;
-    for (int p = lane; p < parts; p += 32)
-      m = fmaxf(m, base0[p * stride + (p == 0) * part_floats(D) + 2 * kTile * D + row]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    float l = 0.f, acc[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const float* part = base0 + p * stride + (p == 0) * part_floats(D);
-      const float lp = part[2 * kTile * D + 2 * kTile + row];
-      const float f = ex2_approx(part[2 * kTile * D + row] - m);
-      if (lp != 0.f) {
-        l = fmaf(f, lp, l);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] = fmaf(f, part[row * D + lane * PER + k], acc[k]);
-      }
-    }
-    const int h = kvh * a.rep + in - jt * a.rep, tk = r.row0 + tok;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (static_cast<size_t>(tk) * a.H + h) * D + lane * PER);
-#pragma unroll
-    for (int k = 0; k < PER / 2; ++k) out[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    if (lane == 0) a.lse[static_cast<size_t>(h) * a.T + tk] = l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994531f;
-  }
-}
-
 template <int D>
 cudaError_t tc_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
                       int grid, cudaStream_t stream) {
@@ -696,11 +531,7 @@ cudaError_t tc_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   cudaError_t e = cudaGetLastError();
   prof_after(stream);
   if (e != cudaSuccess) return e;
-  prof_before(stream, kKernelCacheMerge);
-  s2_cache_join_kernel<D><<<dim3(grid, 8), 256, 0, stream>>>(a);
-  e = cudaGetLastError();
-  prof_after(stream);
-  return e;
+  return launch_join<kPair, kTile, kTile, D>(a, 2 * a.tpt, grid, stream);
 }
 
 }  // namespace

@@ -496,21 +496,21 @@ struct CacheAttnArgs {
   int4* desc;                                       // [grid] items to join
   float* partial;                                   // [2 grid][rows (D + 2)]
   int T, R, H, Hkv, rep, num_blocks, bs_log2, max_blocks;
-  int tpt;                                          // tokens of a 128-row tile: 128 / rep
+  int tpt;                                          // tokens of a row tile (16 or 128 rows)
   float scale_log2;
   uint32_t* status;
   unsigned long long wait_limit_ns;
 };
-constexpr int kCacheRows = 16;     // query rows of a tile (mma.sync kernel)
-constexpr int kCacheMinUnits = 2;  // key tiles a CTA takes at least
-constexpr int kCacheTcGrid = 148;  // CTAs of the tensor-core kernel at most
-constexpr int kCacheGrid = 296;    // CTAs at most (two an SM of 148), which the workspace is sized for
+constexpr int kCacheRows = 16;     // query rows of a tile of the few-row kernel
+constexpr int kCacheMinUnits = 2;  // key tiles a CTA of it takes at least
+constexpr int kCacheSms = 148;     // SMs the workspace is sized for (one CTA each, two of the few-row kernel)
 
 cudaError_t launch_qknorm_fwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
 cudaError_t launch_qknorm_bwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_plan(const CachePlanArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, int D, int grid, cudaStream_t stream);
+cudaError_t launch_cache_dec(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
+                             int D, int grid, cudaStream_t stream);
 cudaError_t launch_cache_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
                             int D, int grid, cudaStream_t stream);
 

@@ -210,7 +210,7 @@ Dims make_segment_dims(int B, int H, int Hkv, int N, int Nk, int D, int causal) 
 // that the per-shape selection would not pick.  It starts from the
 // S2ATTN_TILE environment variable and can be replaced at run time by the
 // s2attn_set_tile_override test hook.  Keys: bwd=split_ds|split|fused, ds_slots=N, bwd_qtile=64|128,
-// fwd_order=snake|pairs, fwd_bn=64|128, fwd_kv=N, bwd_stages=N, nf4_stages=4|5, nf4_dq=8|12.  Unknown
+// fwd_order=snake|pairs, fwd_bn=64|128, fwd_kv=N, bwd_stages=N, nf4_stages=4|5, nf4_dq=8|12, cache=dec|tc.  Unknown
 // keys and values are ignored.
 std::mutex g_override_mu;
 std::string g_override;
@@ -906,6 +906,17 @@ int validate_qknorm(int B, int N, int H, int Hkv, int D, double eps) {
   return S2ATTN_OK;
 }
 
+// Which cache attention kernel a call takes: the one for few rows (at most 16
+// rows of (token, head) per kv head in a tile) while the requests have that
+// many on average, the 128-row tensor-core kernel beyond.  The lengths are
+// device data, so the average is all the host knows; either kernel is right for
+// any lengths.
+bool cache_few_rows(int T, int R, int rep) {
+  const std::string v = override_value(tile_override(), "cache");
+  if (rep > kCacheRows || v == "tc") return false;
+  return v == "dec" || static_cast<long long>(T) * rep <= static_cast<long long>(R) * kCacheRows;
+}
+
 QkNormArgs qknorm_args(const void* q, const void* k, const void* w_q, const void* w_k, const float* table, void* yq,
                        void* yk, int B, int N, int H, int Hkv, double eps) {
   QkNormArgs a = {};
@@ -1149,7 +1160,8 @@ int s2attn_cache_plan(const int* ctx_lens, const int* new_lens, int* block_table
 
 size_t s2attn_cache_attn_workspace_bytes(int D) {
   if (D != 64 && D != 128) return 0;
-  return static_cast<size_t>(kCacheTcGrid) * (sizeof(int4) + 4 * kTile * (D + 2) * sizeof(float));
+  // a descriptor per CTA (two an SM at most) and two parts of 256 rows per SM
+  return kCacheSms * (2 * sizeof(int4) + static_cast<size_t>(4) * kTile * (D + 2) * sizeof(float));
 }
 
 int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_tables,
@@ -1189,7 +1201,7 @@ int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, c
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   a.desc = static_cast<int4*>(workspace);
-  a.partial = reinterpret_cast<float*>(a.desc + kCacheGrid);
+  a.partial = reinterpret_cast<float*>(a.desc + 2 * kCacheSms);
   a.T = T;
   a.R = R;
   a.H = H;
@@ -1201,19 +1213,17 @@ int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, c
   a.scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(D)));
   if (!status_block(&a.status)) return S2ATTN_ERR_CUDA;
   a.wait_limit_ns = wait_limit_ns();
-  a.tpt = kTile / a.rep;
-  if (override_value(tile_override(), "cache") != "mma") {
-    const int rows = block_size < kTile ? block_size : kTile;
-    CUtensorMap tq, tk, tv;
-    if (!make_map(&tq, q, 1, T, H, D, a.tpt, a.rep) || !make_map(&tk, k_cache, 1, num_blocks * block_size, Hkv, D, rows) ||
-        !make_map(&tv, v_cache, 1, num_blocks * block_size, Hkv, D, rows))
-      return S2ATTN_ERR_CUDA;
-    a.partial = reinterpret_cast<float*>(a.desc + kCacheTcGrid);
-    const int grid = info.sms < kCacheTcGrid ? info.sms : kCacheTcGrid;
-    return launched(launch_cache_tc(tq, tk, tv, a, D, grid, static_cast<cudaStream_t>(stream)), 2);
-  }
-  const int grid = 2 * info.sms < kCacheGrid ? 2 * info.sms : kCacheGrid;
-  return launched(launch_cache_attn(a, D, grid, static_cast<cudaStream_t>(stream)), 2);
+  const bool few = cache_few_rows(T, R, a.rep);
+  a.tpt = (few ? kCacheRows : kTile) / a.rep;
+  const int most = few ? 64 : kTile, rows = block_size < most ? block_size : most;  // rows of a page in a key tile
+  CUtensorMap tq, tk, tv;
+  if (!make_map(&tq, q, 1, T, H, D, a.tpt, a.rep) || !make_map(&tk, k_cache, 1, num_blocks * block_size, Hkv, D, rows) ||
+      !make_map(&tv, v_cache, 1, num_blocks * block_size, Hkv, D, rows))
+    return S2ATTN_ERR_CUDA;
+  const int sms = info.sms < kCacheSms ? info.sms : kCacheSms, grid = few ? 2 * sms : sms;
+  const cudaError_t e = few ? launch_cache_dec(tq, tk, tv, a, D, grid, static_cast<cudaStream_t>(stream))
+                            : launch_cache_tc(tq, tk, tv, a, D, grid, static_cast<cudaStream_t>(stream));
+  return launched(e, 2);
 }
 
 size_t s2attn_hga_bwd_workspace_bytes(int B, int H, int Hkv, int N, int D, int G) {

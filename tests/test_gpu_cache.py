@@ -100,6 +100,15 @@ def test_plan_odd_lengths_and_parents():
 
 # ------------------------------------------------------------------ attention
 
+@pytest.fixture(params=["dec", "tc"])
+def kernel(request):
+    """Both attention kernels, whichever the call's sizes would pick."""
+    from sparse_attention_attn_b200 import _lib
+    _lib.s2attn_set_tile_override("cache=" + request.param)
+    yield request.param
+    _lib.s2attn_set_tile_override(None)
+
+
 def _batch(lens, H, Hkv, D, bs, masks, seed, pad=0, spare=2, poison=True):
     """lens: (ctx, new) a request.  Unused rows of the cache hold NaN."""
     rng = np.random.default_rng(seed)
@@ -174,7 +183,7 @@ LENS = {
 
 @pytest.mark.parametrize("H,Hkv,D,bs", [(4, 4, 64, 16), (8, 2, 128, 32), (6, 2, 64, 64), (16, 1, 128, 256)])
 @pytest.mark.parametrize("lens", list(LENS), ids=list(LENS))
-def test_chain_attention_against_oracle(lens, H, Hkv, D, bs):
+def test_chain_attention_against_oracle(kernel, lens, H, Hkv, D, bs):
     b = _batch(LENS[lens], H, Hkv, D, bs, None, 7, pad=3)
     out = torch.full((b["T"], H, D), 5.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((H, b["T"]), 9.0, device="cuda")
@@ -187,7 +196,7 @@ def test_chain_attention_against_oracle(lens, H, Hkv, D, bs):
 
 @pytest.mark.parametrize("H,Hkv,D,bs", [(4, 4, 128, 16), (32, 4, 64, 128), (5, 1, 128, 64)])
 @pytest.mark.parametrize("lens,drop", [("drafts", 0.0), ("ragged", 0.0), ("drafts", 0.4), ("one", 1.0), ("tile-edges", 1.0)])
-def test_tree_attention_against_oracle(lens, drop, H, Hkv, D, bs):
+def test_tree_attention_against_oracle(kernel, lens, drop, H, Hkv, D, bs):
     b = _batch(LENS[lens], H, Hkv, D, bs, _tree_masks(LENS[lens], 3, drop), 11)
     o, l = _call(b)
     torch.cuda.synchronize()
@@ -195,20 +204,20 @@ def test_tree_attention_against_oracle(lens, drop, H, Hkv, D, bs):
     _check(b, o, l)
 
 
-def test_row_without_any_key_is_zero():
+def test_row_without_any_key_is_zero(kernel):
     b = _batch([(0, 3), (0, 1)], 4, 2, 128, 16, [np.array([0, 2, 0], np.uint64), np.array([0], np.uint64)], 13)
     o, l = _call(b)
     assert (o[[0, 2, 3]] == 0).all() and torch.isneginf(l[:, [0, 2, 3]]).all()
     _check(b, o, l)
 
 
-def test_bits_of_drafts_that_do_not_exist_are_ignored():
+def test_bits_of_drafts_that_do_not_exist_are_ignored(kernel):
     b = _batch([(40, 5)], 4, 2, 64, 16, [np.full(5, 0xFFFFFFFFFFFFFFFF, np.uint64)], 14)
     o, l = _call(b)
     _check(b, o, l)
 
 
-def test_same_bits_every_time_and_on_another_stream():
+def test_same_bits_every_time_and_on_another_stream(kernel):
     b = _batch([(4000, 2), (77, 1), (0, 9)], 16, 4, 128, 64, None, 15)
     o, l = _call(b)
     torch.cuda.synchronize()
@@ -220,7 +229,7 @@ def test_same_bits_every_time_and_on_another_stream():
     assert torch.equal(o, o2) and torch.equal(l, l2)
 
 
-def test_blocks_out_of_range_are_reported_and_read_as_zeros():
+def test_blocks_out_of_range_are_reported_and_read_as_zeros(kernel):
     b = _batch([(40, 1), (20, 1)], 4, 2, 64, 16, None, 16)
     good, _ = _call(b)
     torch.cuda.synchronize()
@@ -236,7 +245,7 @@ def test_blocks_out_of_range_are_reported_and_read_as_zeros():
     _check(b, o, l)
 
 
-def test_offsets_beyond_32_bits():
+def test_offsets_beyond_32_bits(kernel):
     """A cache of more than 2^31 elements, the blocks at its far end."""
     Hkv, D, bs, nb = 8, 128, 256, 9000   # 2.36e9 elements each
     b = _batch([(600, 2), (256, 1)], 16, Hkv, D, bs, None, 17, spare=0)
@@ -333,7 +342,7 @@ def test_drafted_tree_matches_its_paths():
         assert np.abs(to64(lse[:, j]) - to64(pl[:, -1])).max() <= 2.0 ** -13
 
 
-def test_captured_step_follows_new_lengths():
+def test_captured_step_follows_new_lengths(kernel):
     """One captured step (plan, append, attention) replayed for growing contexts."""
     H, Hkv, D, bs, R = 8, 2, 128, 16, 3
     kc = I.randn_bf16((64, bs, Hkv, D), 1).cuda()
