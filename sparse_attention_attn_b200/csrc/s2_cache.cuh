@@ -179,95 +179,135 @@ struct Part {
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Joins the parts of the item that begins in CTA blockIdx.x and runs on: block
-// y its rows 8 y .. 8 y + 7.  With few parts each of the 8 warps joins a row,
-// with many all of them share a row's parts.  A part whose row saw no key has
-// l = 0 and nothing else in it.  TILE: rows of a row tile (its first a.tpt
-// tokens); the launch overlaps the attention kernel's end.
-template <int ROWS, int TILE, int KEYS, int D>
-__global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a, int tokens) {
+// The join work of CTA blockIdx.x: an item that begins in it and runs on.
+__device__ __forceinline__ int4 join_work(const Seg& s) {
+  return make_int4(s.row0 + s.tok, s.ntok, s.kvh, s.last_cta);
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.x and runs on.  WPR
+// warps share a row and take every WPR-th part (few rows, many parts: the
+// few-row kernel), or a warp joins RPW rows side by side (many rows, few parts).
+// A part whose row saw no key has l = 0 and may hold anything else: its sums are
+// loaded all the same, so that no load waits for another, and left out.  TILE:
+// rows of a row tile (its first a.tpt tokens).  The launch overlaps the
+// attention kernel's end.
+template <int ROWS, int TILE, int D, int WPR, int RPW>
+__global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a) {
   constexpr int PER = D / 32;  // columns a lane
   __shared__ float share[8][D + 1];
   wait_for_primary();
   const int4 d = a.desc[blockIdx.x];
-  if (d.x < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int kvh = d.y, tok0 = d.z, first = blockIdx.x, parts = d.w - first + 1;
-  const Req r = request<KEYS>(a, d.x, tokens);
-  const int share_of = parts > 8 ? 8 : 1, sub = parts > 8 ? warp : 0;
-  for (int row = blockIdx.y * 8 + (parts > 8 ? 0 : warp); row < blockIdx.y * 8 + 8; row += parts > 8 ? 1 : 8) {
-    const int tile = row / TILE, in = row - tile * TILE, jt = in / a.rep, tok = tok0 + tile * a.tpt + jt;
-    if (jt >= a.tpt || tok >= r.n) continue;  // uniform in the warps that share the row
-    auto part = [&](int p) { return Part<ROWS, D>::at(a, first + p, p == 0 ? 1 : 0); };
-    float m = kFloor;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, part(p)[ROWS * D + row]);
+  if (d.y < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+  const int first = blockIdx.x, parts = d.w - first + 1;
+  const int row0 = (blockIdx.y * (8 / WPR) + warp / WPR) * RPW;
+  if (WPR == 1 && (row0 / TILE) * a.tpt + (row0 % TILE) / a.rep >= d.y) return;  // rows behind the item's
+  auto part = [&](int p) { return Part<ROWS, D>::at(a, first + p, p == 0 ? 1 : 0); };
+  float m[RPW], l[RPW], acc[RPW][PER];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    float l = 0.f, acc[PER];
+  for (int i = 0; i < RPW; ++i) {
+    m[i] = kFloor;
+    l[i] = 0.f;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-    for (int p0 = sub; p0 < parts; p0 += 32 * share_of) {  // this warp's next 32 parts: a lane each for their statistics
-      const int mine = p0 + lane * share_of;
-      const float lp = mine < parts ? part(mine)[ROWS * (D + 1) + row] : 0.f;
-      const float f = lp != 0.f ? ex2_approx(part(mine)[ROWS * D + row] - m) : 0.f;
-      const int n = min(32, (parts - p0 + share_of - 1) / share_of);
+    for (int k = 0; k < PER; ++k) acc[i][k] = 0.f;
+  }
+  // 32 parts of this warp at a time, a lane each for their statistics
+  for (int p0 = sub; p0 < parts; p0 += 32 * WPR) {
+    const int p = p0 + WPR * lane, n = min(32, (parts - p0 + WPR - 1) / WPR);
+    float lp[RPW], f[RPW];
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      lp[i] = p < parts ? part(p)[ROWS * (D + 1) + row0 + i] : 0.f;
+      f[i] = p < parts ? part(p)[ROWS * D + row0 + i] : kFloor;
+    }
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      float mx = lp[i] != 0.f ? f[i] : kFloor;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+      mx = fmaxf(mx, m[i]);
+      const float old = ex2_approx(m[i] - mx);  // the parts before: 1 unless there are more than 32
+      m[i] = mx;
+      l[i] *= old;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) acc[i][k] *= old;
+      f[i] = lp[i] != 0.f ? ex2_approx(f[i] - mx) : 0.f;
+    }
 #pragma unroll 4
-      for (int x = 0; x < n; ++x) {
-        const float lx = __shfl_sync(0xffffffffu, lp, x), fx = __shfl_sync(0xffffffffu, f, x);
-        if (lx != 0.f) {
-          const float* src = part(p0 + x * share_of) + row * D + lane * PER;
-          l = fmaf(fx, lx, l);
-          if constexpr (PER == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            acc[0] = fmaf(fx, v.x, acc[0]);
-            acc[1] = fmaf(fx, v.y, acc[1]);
-            acc[2] = fmaf(fx, v.z, acc[2]);
-            acc[3] = fmaf(fx, v.w, acc[3]);
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            acc[0] = fmaf(fx, v.x, acc[0]);
-            acc[1] = fmaf(fx, v.y, acc[1]);
-          }
-        }
+    for (int x = 0; x < n; ++x) {
+      const float* src = part(p0 + WPR * x) + row0 * D + lane * PER;
+      float v[RPW][PER];
+#pragma unroll
+      for (int i = 0; i < RPW; ++i) {
+        if constexpr (PER == 4)
+          *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(src + i * D);
+        else
+          *reinterpret_cast<float2*>(v[i]) = *reinterpret_cast<const float2*>(src + i * D);
+      }
+#pragma unroll
+      for (int i = 0; i < RPW; ++i) {
+        const float lx = __shfl_sync(0xffffffffu, lp[i], x), fx = __shfl_sync(0xffffffffu, f[i], x);
+        if (lx == 0.f) continue;
+        l[i] = fmaf(fx, lx, l[i]);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[i][k] = fmaf(fx, v[i][k], acc[i][k]);
       }
     }
-    if (parts > 8) {
-      __syncthreads();
+  }
+  if constexpr (WPR > 1) {
+    static_assert(RPW == 1, "warps that share a row join one");
+    __shared__ float share_m[8];
 #pragma unroll
-      for (int k = 0; k < PER; ++k) share[warp][lane * PER + k] = acc[k];
-      if (lane == 0) share[warp][D] = l;
-      __syncthreads();
-      if (warp > 0) continue;
-#pragma unroll
-      for (int w = 1; w < 8; ++w) {
-        l += share[w][D];
-#pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] += share[w][lane * PER + k];
-      }
+    for (int k = 0; k < PER; ++k) share[warp][lane * PER + k] = acc[0][k];
+    if (lane == 0) {
+      share[warp][D] = l[0];
+      share_m[warp] = m[0];
     }
-    const int h = kvh * a.rep + in - jt * a.rep, tk = r.row0 + tok;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (static_cast<size_t>(tk) * a.H + h) * D + lane * PER);
+    __syncthreads();
+    if (sub > 0) return;
+    float mx = m[0];
 #pragma unroll
-    for (int k = 0; k < PER / 2; ++k) out[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    if (lane == 0) a.lse[static_cast<size_t>(h) * a.T + tk] = lse_of(m, l);
+    for (int w = 1; w < WPR; ++w) mx = fmaxf(mx, share_m[warp + w]);
+    const float own = ex2_approx(m[0] - mx);
+    m[0] = mx;
+    l[0] *= own;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[0][k] *= own;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      const float fw = ex2_approx(share_m[warp + w] - mx);
+      l[0] = fmaf(fw, share[warp + w][D], l[0]);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) acc[0][k] = fmaf(fw, share[warp + w][lane * PER + k], acc[0][k]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RPW; ++i) {
+    const int tile = (row0 + i) / TILE, in = row0 + i - tile * TILE, jt = in / a.rep, tok = tile * a.tpt + jt;
+    if (jt >= a.tpt || tok >= d.y) continue;  // a row of no token
+    const int tk = d.x + tok, head = d.z * a.rep + in - jt * a.rep;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (static_cast<size_t>(tk) * a.H + head) * D + lane * PER);
+#pragma unroll
+    for (int k = 0; k < PER / 2; ++k) out[k] = pack_bf16x2(acc[i][2 * k] * inv, acc[i][2 * k + 1] * inv);
+    if (lane == 0) a.lse[static_cast<size_t>(head) * a.T + tk] = lse_of(m[i], l[i]);
   }
 }
 
 // The join as a dependent launch of the attention kernel before it in the stream.
-template <int ROWS, int TILE, int KEYS, int D>
-cudaError_t launch_join(const CacheAttnArgs& a, int tokens, int grid, cudaStream_t stream) {
+template <int ROWS, int TILE, int D, int WPR, int RPW>
+cudaError_t launch_join(const CacheAttnArgs& a, int grid, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, ROWS / 8);
+  cfg.gridDim = dim3(grid, ROWS * WPR / (8 * RPW));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   prof_before(stream, kKernelCacheMerge);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<ROWS, TILE, KEYS, D>, a, tokens);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<ROWS, TILE, D, WPR, RPW>, a);
   prof_after(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   __shared__ Seg segs[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   launch_dependents();
-  if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == 0) a.desc[blockIdx.x] = make_int4(0, -1, 0, 0);
   Run run;
   if (!locate<kDecThreads, kKeys>(a, a.tpt, kCacheMinUnits, sums, found, run)) return;
   const uint32_t sbase = smem_u32(smem);
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           }
         }
         if (lane == 0 && sg.first && !sg.whole)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
-          a.desc[blockIdx.x] = make_int4(sg.ri, sg.kvh, sg.tok, sg.last_cta);
+          a.desc[blockIdx.x] = join_work(sg);
       }
     }
   }
@@ -377,7 +377,7 @@ cudaError_t dec_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   const cudaError_t e = cudaGetLastError();
   prof_after(stream);
   if (e != cudaSuccess) return e;
-  return launch_join<kRows, kRows, kKeys, D>(a, a.tpt, grid, stream);
+  return launch_join<kRows, kRows, D, 4, 1>(a, grid, stream);
 }
 
 }  // namespace

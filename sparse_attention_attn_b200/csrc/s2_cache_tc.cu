@@ -24,8 +24,8 @@
 // is bound by reading the cache; the padding of the 128-row tile is free there
 // (1024 tensor cycles a 64 KB tile against some 2800 of HBM time).
 //
-// Warp roles (320 threads): warp 0 TMA producer (Q ring, K/V ring, the pages of
-// a tile loaded by one lane each), warp 1 UMMA issuer, warps 2-5 softmax A,
+// Warp roles (320 threads): warp 0 TMA producer (segments, Q ring, K/V ring, the
+// pages of a tile loaded by one lane each), warp 1 UMMA issuer, warps 2-5 softmax A,
 // warps 6-9 softmax B, one thread per query row.  P is rounded to bf16 for the
 // product with V; its row sums, the maxima and O stay fp32.  Rows of V behind
 // the last key may hold anything (stale cache rows): the product stops at the
@@ -51,8 +51,9 @@ constexpr int kPair = 2 * kTile;  // rows of an item
 
 template <int D>
 struct TcCfg {
-  static constexpr int NQ = D == 128 ? 3 : 4;       // Q ring
-  static constexpr int NS = D == 128 ? 4 : 8;       // K/V ring
+  static constexpr int NQ = D == 128 ? 2 : 4;       // Q ring
+  static constexpr int NS = D == 128 ? 5 : 10;      // K/V ring
+  static constexpr int NG = 4;                      // segment descriptions
   static constexpr int ATOM = kTile * 128;          // one 64-column slab of a 128-row tile
   static constexpr int TILE = kTile * D * 2;
   static constexpr int OFF_KV = NQ * TILE;
@@ -82,14 +83,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t bar_qfull[NQ], bar_qempty[NQ], bar_full[NS], bar_empty[NS], bar_s[2], bar_plo[2],
-      bar_p[2], bar_o[2], bar_ofree[2], bar_mb, bar_drain;
+      bar_p[2], bar_o[2], bar_ofree[2], bar_mb, bar_drain, bar_gfull[C::NG], bar_gempty[C::NG];
+  __shared__ Seg segs[C::NG];
   __shared__ uint32_t tmem_slot, abort_flag;
   __shared__ long long sums[kThreads / 32], found[2];
   __shared__ float b_m[kTile], b_l[kTile];  // alternating: warpgroup B's row maxima and sums
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   launch_dependents();
-  if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == 0) a.desc[blockIdx.x] = make_int4(0, -1, 0, 0);
   Run run;
   if (!locate<kThreads, kTile>(a, 2 * a.tpt, 1, sums, found, run)) return;
   WaitCtx wc{&abort_flag, a.status, a.wait_limit_ns};
@@ -113,6 +115,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bar_o[i]), 1);
       mbar_init(smem_u32(&bar_ofree[i]), 4);
     }
+    for (int s = 0; s < C::NG; ++s) {
+      mbar_init(smem_u32(&bar_gfull[s]), 1);
+      mbar_init(smem_u32(&bar_gempty[s]), 9);  // the issuer and the softmax warps
+    }
     mbar_init(smem_u32(&bar_mb), 4);
     mbar_init(smem_u32(&bar_drain), 1);
     fence_barrier_init();
@@ -125,14 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  Seg sg;
-  // the next segment; tiles A and B of its item have na and nb tokens (nb = 0: alternating)
-  int na, nb;
-  auto next = [&]() {
-    if (!next_segment<kTile>(a, 2 * a.tpt, run, sg)) return false;
-    na = min(sg.ntok, a.tpt);
-    nb = sg.ntok - na;
-    return true;
+  // The producer walks the segments and hands their descriptions over in a
+  // ring; the other warps keep one until they are done with it (ng: how many
+  // they have had).
+  auto get_seg = [&](int ng, int where) {
+    return warp_wait(smem_u32(&bar_gfull[ng % C::NG]), (ng / C::NG) & 1, wc, where);
+  };
+  auto put_seg = [&](int ng) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar_gempty[ng % C::NG]));
   };
 
   if (warp == 0) {
@@ -143,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmV);
     }
     __syncwarp();
+    Seg sg;
     int qu = 0, L = 0;  // ring uses so far
     bool ok = true;
     const int page_rows = min(1 << a.bs_log2, kTile), page_log2 = min(a.bs_log2, 7);
@@ -173,9 +181,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++L;
       return true;
     };
-    while (ok && next()) {
+    for (int ng = 0; ok; ++ng) {
+      const bool more = next_segment<kTile>(a, 2 * a.tpt, run, sg);
+      if (!more) sg.tiles = -1;
+      const int gs = ng % C::NG;
+      if (ng >= C::NG && !(ok = warp_wait(smem_u32(&bar_gempty[gs]), (ng / C::NG - 1) & 1, wc, 112))) break;
+      if (lane == 0) {
+        segs[gs] = sg;
+        mbar_arrive(smem_u32(&bar_gfull[gs]));
+      }
+      __syncwarp();
+      if (!more) break;
       if (sg.tiles == 0) continue;
-      ok = load_q(sg.row0 + sg.tok) && (nb == 0 || load_q(sg.row0 + sg.tok + a.tpt));
+      ok = load_q(sg.row0 + sg.tok) && (sg.ntok <= a.tpt || load_q(sg.row0 + sg.tok + a.tpt));
       const int* table = a.block_tables + static_cast<size_t>(sg.ri) * a.max_blocks;
       for (int i = 0; ok && i < sg.tiles; ++i) {
         const int key = (sg.kt0 + i) * kTile + (lane << page_log2);
@@ -222,38 +240,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     int L = 0, qu = 0, np[2] = {0, 0}, nseg[2] = {0, 0};
-    // O_wg (+)= P_wg V(load Lv) over the 16-key steps [k0, k1) of the tile
-    auto issue_pv = [&](int wg, int Lv, int k0, int k1, bool acc) {
+    // O_wg (+)= P_wg V(load Lv), half h of the tile's keys, as far as there are
+    // nk 16-key steps with a key; the second half completes the product (bar_o)
+    auto issue_pv = [&](int wg, int Lv, int h, int nk, bool acc) {
       tc_fence_after();
       const uint64_t dv = sdesc_advance(dV0, (Lv % NS) * C::TILE);
-      if (elect_one())
-        for (int kk = k0; kk < k1; ++kk)
-          umma_ts(tmem + (wg ? C::TM_OB : C::TM_O), tmem + wg * 128 + kk * 8, sdesc_advance(dv, kk * 2048), idO,
-                  acc || kk > 0);
+      if (elect_one()) {
+#pragma unroll
+        for (int kq = 0; kq < kTile / 32; ++kq) {
+          const int kk = h * (kTile / 32) + kq;
+          if (kk < nk)
+            umma_ts(tmem + (wg ? C::TM_OB : C::TM_O), tmem + wg * 128 + kk * 8, sdesc_advance(dv, kk * 2048), idO,
+                    acc || kk > 0);
+        }
+        if (h == 1) umma_commit(smem_u32(&bar_o[wg]));
+      }
       __syncwarp();
     };
-    // step j of warpgroup wg: P V of key tile t, keys 0..63 as soon as they are there
-    auto pv = [&](int wg, int Lv, int j, int t) -> bool {
-      const int nk = (min(sg.keys - t * kTile, kTile) + 15) >> 4;  // 16-key steps with a key
+    // step j of warpgroup wg: P V, keys 0..63 as soon as they are there
+    auto pv = [&](int wg, int Lv, int j, int nk) -> bool {
       if (!warp_wait(smem_u32(&bar_plo[wg]), np[wg] & 1, wc, 122 + wg)) return false;
       if (j == 0 && nseg[wg] > 0 && !warp_wait(smem_u32(&bar_ofree[wg]), (nseg[wg] - 1) & 1, wc, 124 + wg)) return false;
       if (!wait_full(Lv)) return false;
-      issue_pv(wg, Lv, 0, min(nk, 4), j > 0);
+      issue_pv(wg, Lv, 0, nk, j > 0);
       if (!warp_wait(smem_u32(&bar_p[wg]), np[wg] & 1, wc, 126 + wg)) return false;
-      issue_pv(wg, Lv, 4, nk, true);
-      commit(&bar_o[wg]);
+      issue_pv(wg, Lv, 1, nk, true);
       ++np[wg];
       return true;
     };
     bool ok = true;
-    while (ok && next()) {
-      if (sg.tiles == 0) continue;
-      const bool alt = nb == 0;
-      const int n = sg.tiles, nA = alt ? (n + 1) / 2 : n, nB = alt ? n / 2 : n;
+    for (int ng = 0; ok; ++ng) {
+      if (!(ok = get_seg(ng, 128))) break;
+      const Seg& sg = segs[ng % C::NG];
+      const int n = sg.tiles, kt0 = sg.kt0, keys = sg.keys;
+      const bool alt = sg.ntok <= a.tpt;
+      put_seg(ng);
+      if (n < 0) break;
+      if (n == 0) continue;
+      const int nA = alt ? (n + 1) / 2 : n, nB = alt ? n / 2 : n;
       const int qa = qu % NQ, qb = alt ? qa : (qu + 1) % NQ, L0 = L;
-      // load of the K tile of step j (its V tile is the next load), and the key tile
+      // load of the K tile of step j (its V tile is the next load), and the
+      // 16-key steps of its key tile that hold a key
       auto lk = [&](int wg, int j) { return L0 + (alt ? 4 * j + 2 * wg : 2 * j); };
-      auto tile = [&](int wg, int j) { return sg.kt0 + (alt ? 2 * j + wg : j); };
+      auto steps16 = [&](int wg, int j) {
+        return (min(keys - (kt0 + (alt ? 2 * j + wg : j)) * kTile, kTile) + 15) >> 4;
+      };
       ok = warp_wait(smem_u32(&bar_qfull[qa]), (qu / NQ) & 1, wc, 121) &&
            (alt || warp_wait(smem_u32(&bar_qfull[qb]), ((qu + 1) / NQ) & 1, wc, 121)) && wait_full(lk(0, 0));
       if (!ok) break;
@@ -265,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(&bar_empty[lk(1, 0) % NS]);
       }
       for (int j = 0; ok && j < nA; ++j) {
-        if (!(ok = pv(0, lk(0, j) + 1, j, tile(0, j)))) break;
+        if (!(ok = pv(0, lk(0, j) + 1, j, steps16(0, j)))) break;
         if (alt) commit(&bar_empty[(lk(0, j) + 1) % NS]);
         if (j + 1 < nA) {
           if (!(ok = wait_full(lk(0, j + 1)))) break;
@@ -273,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (alt) commit(&bar_empty[lk(0, j + 1) % NS]);
         }
         if (j < nB) {
-          if (!(ok = pv(1, lk(1, j) + 1, j, tile(1, j)))) break;
+          if (!(ok = pv(1, lk(1, j) + 1, j, steps16(1, j)))) break;
           commit(&bar_empty[(lk(1, j) + 1) % NS]);
           if (j + 1 < nB) {
             if (alt && !(ok = wait_full(lk(1, j + 1)))) break;
@@ -301,52 +332,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + wg * 128;
-    const uint32_t tOA = tmem + lane_off + C::TM_O, tOB = tmem + lane_off + C::TM_OB;
-    const uint32_t tO = wg ? tOB : tOA;
+    const uint32_t tO = tS + C::TM_O;  // O_B lies 128 columns behind O_A, as S_B behind S_A
     const float sl2 = a.scale_log2;
-    int ns = 0, no[2] = {0, 0}, nmb = 0, L = 0;  // phases so far; K/V ring loads consumed
+    int ns = 0, nsb = 0, nmb = 0, L = 0;  // phases so far (S and P V go together; A counts B's); K/V ring loads consumed
     bool ok = true;
-    while (ok && next()) {
-      const bool alt = nb == 0;
-      const int n = sg.tiles, nA = alt ? (n + 1) / 2 : n, nB = alt ? n / 2 : n, steps = wg ? nB : nA;
-      const int L0 = L;
+    for (int ng = 0; ok; ++ng) {
+      if (!(ok = get_seg(ng, 129))) break;
+      const Seg& sg = segs[ng % C::NG];  // read where it is needed: registers are short
+      const int n = sg.tiles;
+      if (n < 0) break;
+      const bool alt = sg.ntok <= a.tpt;
+      const int steps = alt ? (n + 1 - wg) / 2 : n, ctx = sg.ctx;
       L += 2 * n;
-      const bool second = wg == 1 && !alt;                // this warpgroup works on tile B
-      const int ntok = second ? nb : na, tok = sg.tok + (second ? a.tpt : 0);
-      const int jt = row / a.rep, g = row - jt * a.rep;  // token in the tile, head in the group
-      const bool live = row < ntok * a.rep, busy = quarter * 32 < ntok * a.rep;  // busy: the warp has a live row
-      const int j_tok = tok + jt, gtok = sg.row0 + j_tok, head = sg.kvh * a.rep + g;
-      // the drafts this row sees, as bits (masks), or the last of them (chains)
-      unsigned long long see = 0;
-      if (a.mask != nullptr && live) see = visible_drafts(a, sg, gtok);
-      const int last_key = min(sg.ctx + j_tok, sg.keys - 1);  // chains
+      // the warp has a live row
+      const bool busy = quarter * 32 < (alt || wg == 0 ? min(sg.ntok, a.tpt) : sg.ntok - a.tpt) * a.rep;
       float m_run = kFloor, l_run = 0.f;
-      for (int j = 0; j < steps; ++j) {
-        const int t = sg.kt0 + (alt ? 2 * j + wg : j), key0 = t * kTile;
-        const int valid = min(sg.keys - key0, kTile);
+      int key0 = (sg.kt0 + (alt ? wg : 0)) * kTile;
+      for (int j = 0; j < steps; ++j, key0 += alt ? 2 * kTile : kTile) {
         ok = warp_wait(smem_u32(&bar_s[wg]), ns & 1, wc, 130);
         if (!ok) break;
         ++ns;
-        if ((valid & 15) != 0 && (alt || wg == 0)) {
-          // rows of V behind the last key, within its 16-key step: zero.  (After
-          // the wait for S: the slot's earlier tile has been used by then, so
-          // the wait below cannot mistake its phase.)
-          const int Lv = L0 + (alt ? 4 * j + 2 * wg : 2 * j) + 1;
-          ok = warp_wait(smem_u32(&bar_full[Lv % NS]), (Lv / NS) & 1, wc, 133);
-          if (!ok) break;
-          const int rows = 16 - (valid & 15);
-          for (int e = row; e < rows * (D / 8); e += 128) {
-            const int r = valid + e / (D / 8), c = e % (D / 8);
-            st_shared_v4(kv_addr(Lv % NS) + (c >> 3) * C::ATOM + r * 128 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
+        const bool edge = key0 + kTile > ctx;  // drafts, or keys behind the last, in this tile
+        if (edge && (alt || wg == 0)) {
+          const int valid = min(sg.keys - key0, kTile);
+          if ((valid & 15) != 0) {
+            // rows of V behind the last key, within its 16-key step: zero.  (After
+            // the wait for S: the slot's earlier tile has been used by then, so
+            // the wait below cannot mistake its phase.)
+            const int Lv = L - 2 * n + (alt ? 4 * j + 2 * wg : 2 * j) + 1;
+            ok = warp_wait(smem_u32(&bar_full[Lv % NS]), (Lv / NS) & 1, wc, 133);
+            if (!ok) break;
+            const int rows = 16 - (valid & 15);
+            for (int e = row; e < rows * (D / 8); e += 128) {
+              const int r = valid + e / (D / 8), c = e % (D / 8);
+              st_shared_v4(kv_addr(Lv % NS) + (c >> 3) * C::ATOM + r * 128 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
         }
         if (!busy) {  // no live row: only the protocol
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bar_plo[wg]));
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bar_p[wg]));
-          ++no[wg];
           continue;
         }
         tc_fence_after();
@@ -354,15 +382,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
         tmem_wait_ld();
-        if (key0 + kTile > sg.ctx) {  // drafts, or keys behind the last, in this tile
+        if (edge) {
+          // (the row's token is worked out here, for the one or two such tiles of a segment)
+          const int j_tok = sg.tok + (alt || wg == 0 ? 0 : a.tpt) + row / a.rep;
           if (a.mask == nullptr) {
-            const int lim = last_key - key0;  // last visible column
+            const int lim = min(ctx + j_tok, sg.keys - 1) - key0;  // last visible column
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(neg_inf());
           } else {
-            // visible columns as 4 words: cached keys, then the draft bits
-            const int d0 = sg.ctx - key0;  // column of draft 0 (below 0: drafts begin in an earlier tile)
+            // visible columns as 4 words: cached keys, then the draft bits (of the request's rows)
+            const unsigned long long see = j_tok < sg.tok + sg.ntok ? visible_drafts(a, sg, sg.row0 + j_tok) : 0ull;
+            const int d0 = ctx - key0;  // column of draft 0 (below 0: drafts begin in an earlier tile)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const int at = d0 - 32 * w;  // draft 0 relative to this word
@@ -404,17 +435,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st16(tS + 16, pk);
         if (__any_sync(0xffffffffu, resc)) {
           // O holds P V up to the previous step once that UMMA has completed
-          ok = warp_wait(smem_u32(&bar_o[wg]), (no[wg] - 1) & 1, wc, 131);
+          ok = warp_wait(smem_u32(&bar_o[wg]), ns & 1, wc, 131);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + c * 16, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tO + c * 32, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(tO + c * 16, o);
           }
         }
         tmem_wait_st();
@@ -430,11 +461,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_p[wg]));
-        ++no[wg];
       }
       if (!ok) break;
-      if (wg == 0) no[1] += nB;  // warpgroup B's products, which A waits for when it joins them
+      const int nB = alt ? n / 2 : n;
+      nsb += nB;  // warpgroup B's products, which A waits for when it joins them
       // ---------------------------------------------------------- epilogue
+      int erow = row;
+      asm volatile("" : "+r"(erow));  // (computed here again rather than held through the loop)
+      const bool second = wg == 1 && !alt;  // this warpgroup worked on tile B
+      const int jt = erow / a.rep, gtok = sg.row0 + sg.tok + (second ? a.tpt : 0) + jt;
+      const int head = sg.kvh * a.rep + erow - jt * a.rep;
+      const bool live = jt < (second ? sg.ntok - a.tpt : min(sg.ntok, a.tpt));
       // where the row goes: o and lse, or this CTA's part (0: the item began before, 1: it begins here)
       float* part = Part<kPair, D>::at(a, blockIdx.x, sg.first);
       const int prow = (second ? kTile : 0) + row;
@@ -449,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (steps > 0) {
-        ok = warp_wait(smem_u32(&bar_o[wg]), (no[wg] - 1) & 1, wc, 132);
+        ok = warp_wait(smem_u32(&bar_o[wg]), (ns - 1) & 1, wc, 132);
         if (!ok) break;
         tc_fence_after();
       }
@@ -462,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (alt && nB > 0) {
         ok = warp_wait(smem_u32(&bar_mb), nmb & 1, wc, 134) &&
-             warp_wait(smem_u32(&bar_o[1]), (no[1] - 1) & 1, wc, 135);
+             warp_wait(smem_u32(&bar_o[1]), (nsb - 1) & 1, wc, 135);
         if (!ok) break;
         ++nmb;
         tc_fence_after();
@@ -473,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t va[32], vb[32];
-            tmem_ld32(tOA + c * 32, va);
-            tmem_ld32(tOB + c * 32, vb);
+            tmem_ld32(tO + c * 32, va);
+            tmem_ld32(tO + 128 + c * 32, vb);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -508,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         finish(m_run, l_run);
       }
       if (sg.first && !sg.whole && wg == 0 && row == 0)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
-        a.desc[blockIdx.x] = make_int4(sg.ri, sg.kvh, sg.tok, sg.last_cta);
+        a.desc[blockIdx.x] = join_work(sg);
+      put_seg(ng);
     }
   }
 
@@ -531,7 +569,7 @@ cudaError_t tc_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   cudaError_t e = cudaGetLastError();
   prof_after(stream);
   if (e != cudaSuccess) return e;
-  return launch_join<kPair, kTile, kTile, D>(a, 2 * a.tpt, grid, stream);
+  return launch_join<kPair, kTile, D, 1, 4>(a, grid, stream);
 }
 
 }  // namespace

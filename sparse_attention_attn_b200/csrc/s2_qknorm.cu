@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(256) s2_qknorm_fwd_kernel(QkNormArgs a) {
 // a time; a thread keeps the sums of du r x of its 16 columns in registers,
 // and the block leaves one partial row per weight in the workspace.
 template <int D, typename W, int HG>
-__global__ void __launch_bounds__(256) s2_qknorm_bwd_kernel(QkNormArgs a) {
+__global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
   constexpr int CH = D / 16;
   __shared__ float red[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = lane % CH;

@@ -27,6 +27,9 @@ class Bar:
                 self.rem = self.count
 
 
+NG = 4  # segment descriptions
+
+
 def run(segs, seed, NQ=3, NS=4, early_zero=False):
     rnd = random.Random(seed)
     bars = {}
@@ -38,6 +41,9 @@ def run(segs, seed, NQ=3, NS=4, early_zero=False):
         for name, cnt in (("s", 1), ("plo", 4), ("p", 4), ("o", 1), ("ofree", 4)):
             bars[(name, w)] = Bar(cnt)
     bars[("mb", 0)] = Bar(4)
+    for s in range(NG):
+        bars[("gfull", s)], bars[("gempty", s)] = Bar(1), Bar(9)
+    descr, users = [None] * NG, [0] * NG     # segment descriptions, and who still needs them
     err, tma, pipe = [], [], []
     qslot, qreads, ring, ringreads = [None] * NQ, [0] * NQ, [None] * NS, [0] * NS
     sbuf = [[None] * 4, [None] * 4]          # per warp quarter: what its lanes of S/P hold
@@ -50,9 +56,24 @@ def run(segs, seed, NQ=3, NS=4, early_zero=False):
     def key_tile(k, w, j):
         return j if segs[k][1] else 2 * j + w
 
+    def take(k):
+        yield ("wait", ("gfull", k % NG), k // NG)
+        if descr[k % NG] != k:
+            err.append(f"segment {descr[k % NG]} for {k}")
+
+    def give(k):
+        users[k % NG] -= 1
+        return ("arrive", ("gempty", k % NG), 1)
+
     def producer():
         qu = L = 0
         for k, (n, paired, _) in enumerate(segs):
+            if k >= NG:
+                yield ("wait", ("gempty", k % NG), k // NG - 1)
+            if users[k % NG]:
+                err.append("segment description overwritten")
+            descr[k % NG], users[k % NG] = k, 9
+            yield ("arrive", ("gfull", k % NG), 1)
             if n == 0:
                 continue
             _, nA, nB = shape(k)
@@ -92,6 +113,8 @@ def run(segs, seed, NQ=3, NS=4, early_zero=False):
             return ("wait", ("full", Lx % NS), Lx // NS)
 
         for k, (n, paired, _) in enumerate(segs):
+            yield from take(k)
+            yield give(k)
             if n == 0:
                 continue
             alt = not paired
@@ -161,6 +184,7 @@ def run(segs, seed, NQ=3, NS=4, early_zero=False):
         ns = L = nmb = 0
         no = [0, 0]
         for k, (n, paired, ragged) in enumerate(segs):
+            yield from take(k)
             alt = not paired
             _, nA, nB = shape(k)
             steps, L0 = (nA, nB)[w], L
@@ -216,6 +240,9 @@ def run(segs, seed, NQ=3, NS=4, early_zero=False):
             elif steps > 0:
                 o_read.add((w, k, quarter))
                 yield ("arrive", ("ofree", w), 1)
+            if descr[k % NG] != k:
+                err.append("segment description replaced in use")
+            yield give(k)
 
     def execute():
         op = pipe.pop(0)
