@@ -159,6 +159,14 @@ __device__ __forceinline__ unsigned long long visible_drafts(const CacheAttnArgs
   return a.mask[token] & (drafts >= 64 ? ~0ull : (1ull << drafts) - 1ull);
 }
 
+// Whether one of two / eight bf16 values is infinite or NaN (all exponent bits set).
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool nonfinite8(const uint4& u) {
+  return nonfinite2(u.x) || nonfinite2(u.y) || nonfinite2(u.z) || nonfinite2(u.w);
+}
+
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994531f;
 }

@@ -264,19 +264,52 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               keep[x] = (key < sg.keys ? 0xffffu : 0u) | (key + 1 < sg.keys ? 0xffff0000u : 0u);
             }
           }
-          const int vrow = warp * 16 + (lane & 15);
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            uint32_t b[4];
-            ldsm4t(b, swz(sv, C::SLAB, vrow, 2 * d + (lane >> 4)));
-            if (ragged) {
-              b[0] &= keep[0];
-              b[1] &= keep[1];
-              b[2] &= keep[0];
-              b[3] &= keep[1];
+          // A product adds 0 V for the keys a row does not see, which is not 0
+          // where V is infinite or NaN: drafts are looked through for such
+          // values, and added without the matrix units where there are any.
+          bool odd = false;
+          if (key0 + 16 > sg.ctx && (a.mask != nullptr || sg.keys - sg.ctx > 1)) {
+            for (int e = lane; e < 16 * (D / 8); e += 32) {
+              const int r = e / (D / 8);
+              if (key0 + r < sg.keys) odd |= nonfinite8(lds_u4(swz(sv, C::SLAB, warp * 16 + r, e % (D / 8))));
             }
-            mma16816(o[2 * d], pf, b[0], b[1]);
-            mma16816(o[2 * d + 1], pf, b[2], b[3]);
+            odd = __any_sync(0xffffffffu, odd);
+          }
+          if (odd) {
+            for (int key = 0; key < 16 && key0 + key < sg.keys; ++key) {
+              float p[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w = __shfl_sync(0xffffffffu, key < 8 ? pf[h] : pf[h + 2], (lane & ~3) | ((key & 7) >> 1));
+                p[h] = __uint_as_float(key & 1 ? w & 0xffff0000u : w << 16);
+              }
+#pragma unroll
+              for (int d = 0; d < D / 8; ++d) {
+                uint32_t w;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(swz(sv, C::SLAB, warp * 16 + key, d) + (lane & 3) * 4));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  if (p[h] == 0.f) continue;  // not seen
+                  o[d][2 * h] = fmaf(p[h], __uint_as_float(w << 16), o[d][2 * h]);
+                  o[d][2 * h + 1] = fmaf(p[h], __uint_as_float(w & 0xffff0000u), o[d][2 * h + 1]);
+                }
+              }
+            }
+          } else {
+            const int vrow = warp * 16 + (lane & 15);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              uint32_t b[4];
+              ldsm4t(b, swz(sv, C::SLAB, vrow, 2 * d + (lane >> 4)));
+              if (ragged) {
+                b[0] &= keep[0];
+                b[1] &= keep[1];
+                b[2] &= keep[0];
+                b[3] &= keep[1];
+              }
+              mma16816(o[2 * d], pf, b[0], b[1]);
+              mma16816(o[2 * d + 1], pf, b[2], b[3]);
+            }
           }
         }
         __syncwarp();

@@ -30,7 +30,8 @@
 // product with V; its row sums, the maxima and O stay fp32.  Rows of V behind
 // the last key may hold anything (stale cache rows): the product stops at the
 // 16-key step that holds the last key, and the rows of that step behind it are
-// zeroed in shared memory first.
+// zeroed in shared memory first, as are infinite and NaN values of drafts,
+// which only the rows that see them may get.
 //
 // TMEM (512 columns): S_A [0,128), S_B [128,256) (P over their first 64
 // columns), O_A [256, 256+D), O_B [384, 384+D).
@@ -73,10 +74,34 @@ __device__ __forceinline__ void store_o32(__nv_bfloat16* o, float* part, bool wh
   }
 }
 
+// Adds the infinite and NaN values of V in the segment's drafts to the stored
+// row (o, or its part) of a token that sees them; any weight turns such a value
+// into itself.  Out of line: such values are an error of the model's.
+template <int D>
+__device__ __noinline__ void add_odd(const CacheAttnArgs& a, const Seg& sg, int token, __nv_bfloat16* o, float* part) {
+  const int j_tok = token - sg.row0, last = min((sg.kt0 + sg.tiles) * kTile, sg.keys);
+  const unsigned long long see = a.mask != nullptr ? visible_drafts(a, sg, token) : 0ull;
+  for (int key = max(sg.kt0 * kTile, sg.ctx); key < last; ++key) {
+    const int d = key - sg.ctx, blk = a.block_tables[static_cast<size_t>(sg.ri) * a.max_blocks + (key >> a.bs_log2)];
+    if (a.mask != nullptr ? d >= 64 || !(see >> d & 1) : d > j_tok) continue;
+    if (blk < 0 || blk >= a.num_blocks) continue;
+    const size_t place = (static_cast<size_t>(blk) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1));
+    const __nv_bfloat16* src = a.v_cache + (place * a.Hkv + sg.kvh) * D;
+    for (int i = 0; i < D; ++i) {
+      const float x = __bfloat162float(src[i]);
+      if (isfinite(x)) continue;
+      if (sg.whole)
+        o[i] = __float2bfloat16(__bfloat162float(o[i]) + x);
+      else
+        part[i] += x;
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     s2_cache_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a) {
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CacheAttnArgs a) {
   using C = TcCfg<D>;
   constexpr int NQ = C::NQ, NS = C::NS;
   extern __shared__ unsigned char smem_raw[];
@@ -85,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_qfull[NQ], bar_qempty[NQ], bar_full[NS], bar_empty[NS], bar_s[2], bar_plo[2],
       bar_p[2], bar_o[2], bar_ofree[2], bar_mb, bar_drain, bar_gfull[C::NG], bar_gempty[C::NG];
   __shared__ Seg segs[C::NG];
+  __shared__ uint32_t odd[C::NG];  // the segment's drafts hold infinite or NaN values
   __shared__ uint32_t tmem_slot, abort_flag;
   __shared__ long long sums[kThreads / 32], found[2];
   __shared__ float b_m[kTile], b_l[kTile];  // alternating: warpgroup B's row maxima and sums
@@ -188,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ng >= C::NG && !(ok = warp_wait(smem_u32(&bar_gempty[gs]), (ng / C::NG - 1) & 1, wc, 112))) break;
       if (lane == 0) {
         segs[gs] = sg;
+        odd[gs] = 0;
         mbar_arrive(smem_u32(&bar_gfull[gs]));
       }
       __syncwarp();
@@ -354,18 +381,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
         const bool edge = key0 + kTile > ctx;  // drafts, or keys behind the last, in this tile
         if (edge && (alt || wg == 0)) {
-          const int valid = min(sg.keys - key0, kTile);
-          if ((valid & 15) != 0) {
-            // rows of V behind the last key, within its 16-key step: zero.  (After
-            // the wait for S: the slot's earlier tile has been used by then, so
-            // the wait below cannot mistake its phase.)
+          const bool hides = a.mask != nullptr || sg.keys - ctx > 1;  // some row may not see some draft
+          const int valid = min(sg.keys - key0, kTile), drafts = hides ? valid - max(ctx - key0, 0) : 0;
+          if ((valid & 15) != 0 || drafts > 0) {
+            // (After the wait for S: the slot's earlier tile has been used by
+            // then, so this wait cannot mistake its phase.)
             const int Lv = L - 2 * n + (alt ? 4 * j + 2 * wg : 2 * j) + 1;
             ok = warp_wait(smem_u32(&bar_full[Lv % NS]), (Lv / NS) & 1, wc, 133);
             if (!ok) break;
-            const int rows = 16 - (valid & 15);
+            // Rows of V behind the last key, within its 16-key step, are zeroed.
+            // So are infinite and NaN values of drafts, which a product would
+            // add as 0 V to rows that do not see them: add_odd adds them to the
+            // rows that do.
+            const int rows = drafts + (-valid & 15);
             for (int e = row; e < rows * (D / 8); e += 128) {
-              const int r = valid + e / (D / 8), c = e % (D / 8);
-              st_shared_v4(kv_addr(Lv % NS) + (c >> 3) * C::ATOM + r * 128 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
+              const int r = valid - drafts + e / (D / 8), c = e % (D / 8);
+              const uint32_t at = kv_addr(Lv % NS) + (c >> 3) * C::ATOM + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              if (r < valid) {
+                w = lds_u4(at);
+                if (!nonfinite8(w)) continue;
+                odd[ng % C::NG] = 1;
+                uint32_t* h = &w.x;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  if ((h[x] & 0x7f80u) == 0x7f80u) h[x] &= 0xffff0000u;
+                  if ((h[x] & 0x7f800000u) == 0x7f800000u) h[x] &= 0xffffu;
+                }
+              }
+              st_shared_v4(at, w.x, w.y, w.z, w.w);
             }
             fence_proxy_async_smem();
           }
@@ -484,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[kPair * D + prow] = m;
           part[kPair * (D + 1) + prow] = l;
         }
+        if (odd[ng % C::NG]) add_odd<D>(a, sg, gtok, orow, part + prow * D);
       };
       if (steps > 0) {
         ok = warp_wait(smem_u32(&bar_o[wg]), (ns - 1) & 1, wc, 132);
@@ -569,7 +614,7 @@ cudaError_t tc_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   cudaError_t e = cudaGetLastError();
   prof_after(stream);
   if (e != cudaSuccess) return e;
-  return launch_join<kPair, kTile, D, 1, 4>(a, grid, stream);
+  return launch_join<kPair, kTile, D, 1, 2>(a, grid, stream);
 }
 
 }  // namespace

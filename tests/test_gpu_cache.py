@@ -211,6 +211,37 @@ def test_row_without_any_key_is_zero(kernel):
     _check(b, o, l)
 
 
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 4, 64), (8, 2, 128), (16, 1, 128)])
+def test_non_finite_drafts_reach_only_the_rows_that_see_them(kernel, H, Hkv, D, tree):
+    lens = [(37, 6), (126, 5), (0, 2), (255, 1), (70, 40)]
+    masks = _tree_masks(lens, 5) if tree else None
+    if tree:
+        masks[2] = np.array([2, 1], np.uint64)   # each sees the other one only
+        masks[3] = np.array([0], np.uint64)      # sees the context only
+    b = _batch(lens, H, Hkv, D, 16, masks, 19)
+    for r, (c, n) in enumerate(lens):
+        k, v = b["reqs"][r]
+        for j, col, x in ((n - 1, 3, float("nan")), (n // 2, 10, float("inf")), (n // 2, D - 1, -float("inf"))):
+            v[c + j, -1, col] = x
+        if n > 5:
+            k[c + 4, 0, 7] = float("nan")        # the scores of those that see it
+        p = np.arange(c + n)
+        b["kc"][b["tab"][r, p // 16], p % 16], b["vc"][b["tab"][r, p // 16], p % 16] = k, v
+    o, l = (to64(x) for x in _call(b))
+    for r, (c, n) in enumerate(lens):
+        t0 = b["cu"][r]
+        with np.errstate(invalid="ignore"):
+            want, want_l, mag = cr.attention(to64(b["q"])[t0:t0 + n], *(to64(x) for x in b["reqs"][r]), c,
+                                             cr.visible(n, None if masks is None else masks[r]))
+        got = o[t0:t0 + n]
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isposinf(got), np.isposinf(want))
+        assert np.array_equal(np.isneginf(got), np.isneginf(want))
+        fine = np.isfinite(want)
+        assert np.all(np.abs(got - want)[fine] <= (2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -12) * mag)[fine])
+        assert np.array_equal(np.isnan(l[:, t0:t0 + n]), np.isnan(want_l))
+
+
 def test_bits_of_drafts_that_do_not_exist_are_ignored(kernel):
     b = _batch([(40, 5)], 4, 2, 64, 16, [np.full(5, 0xFFFFFFFFFFFFFFFF, np.uint64)], 14)
     o, l = _call(b)
