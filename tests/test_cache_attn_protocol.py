@@ -30,7 +30,7 @@ class Bar:
 NG = 4  # segment descriptions
 
 
-def run(segs, seed, NQ=3, NS=4, early_zero=False):
+def run(segs, seed, NQ=2, NS=5, early_zero=False):
     rnd = random.Random(seed)
     bars = {}
     for s in range(NQ):
@@ -329,7 +329,7 @@ def sequences():
     return out
 
 
-@pytest.mark.parametrize("NQ,NS", [(3, 4), (4, 8)])
+@pytest.mark.parametrize("NQ,NS", [(2, 5), (4, 10)])
 def test_cache_attention_protocol_runs_clean(NQ, NS):
     for segs in sequences():
         for seed in range(8):
@@ -338,5 +338,5 @@ def test_cache_attention_protocol_runs_clean(NQ, NS):
 
 
 def test_model_finds_rows_zeroed_too_early():
-    """Zeroing before the wait for S mistakes the slot's earlier tile: the check is not vacuous."""
-    assert any(run([(5, False, True)], seed, early_zero=True) for seed in range(40))
+    """Zeroing before the wait for S mistakes the slot's earlier tile in a four-slot ring: the check is not vacuous."""
+    assert any(run([(5, False, True)], seed, 3, 4, early_zero=True) for seed in range(40))

@@ -238,7 +238,8 @@ def test_non_finite_drafts_reach_only_the_rows_that_see_them(kernel, H, Hkv, D, 
         assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isposinf(got), np.isposinf(want))
         assert np.array_equal(np.isneginf(got), np.isneginf(want))
         fine = np.isfinite(want)
-        assert np.all(np.abs(got - want)[fine] <= (2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -12) * mag)[fine])
+        g, w = got[fine], want[fine]
+        assert np.all(np.abs(g - w) <= 2.0 ** -8 * np.abs(w) + (2.0 ** -8 + 2.0 ** -12) * mag[fine])
         assert np.array_equal(np.isnan(l[:, t0:t0 + n]), np.isnan(want_l))
 
 
