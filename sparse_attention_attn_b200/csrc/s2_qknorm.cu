@@ -28,35 +28,42 @@ namespace s2 {
 
 namespace {
 
-// 8 weights of one half at w + off, as fp32.
-__device__ __forceinline__ void load_w8(const float* w, int off, float (&o)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(w + off), b = *reinterpret_cast<const float4*>(w + off + 4);
-  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
-}
-__device__ __forceinline__ void unpack8(const uint4& u, float (&o)[8]) {
+// An octet of values as 4 packed pairs: the arithmetic runs on pairs
+// (fma.rn.f32x2), which halves its instructions; on single floats the backward
+// filled half of the issue slots and reached 66% of the DRAM's cycles.
+struct Oct {
+  uint64_t v[4];
+};
+__device__ __forceinline__ Oct unpack8(const uint4& u) {
   const uint32_t p[4] = {u.x, u.y, u.z, u.w};
+  Oct o;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&p[j]));
-    o[2 * j] = f.x;
-    o[2 * j + 1] = f.y;
-  }
+  for (int j = 0; j < 4; ++j) o.v[j] = f2_pack(__uint_as_float(p[j] << 16), __uint_as_float(p[j] & 0xffff0000u));
+  return o;
 }
-__device__ __forceinline__ void load_w8(const __nv_bfloat16* w, int off, float (&o)[8]) {
-  unpack8(*reinterpret_cast<const uint4*>(w + off), o);
+__device__ __forceinline__ uint4 pack8(const Oct& f) {
+  return make_uint4(f2_to_bf16x2(f.v[0]), f2_to_bf16x2(f.v[1]), f2_to_bf16x2(f.v[2]), f2_to_bf16x2(f.v[3]));
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+// 8 weights of one half at w + off, as fp32.
+__device__ __forceinline__ Oct load_w8(const float* w, int off) {
+  const float4 a = *reinterpret_cast<const float4*>(w + off), b = *reinterpret_cast<const float4*>(w + off + 4);
+  return {{f2_pack(a.x, a.y), f2_pack(a.z, a.w), f2_pack(b.x, b.y), f2_pack(b.z, b.w)}};
 }
-__device__ __forceinline__ void load_turn(const float2* table, size_t off, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ Oct load_w8(const __nv_bfloat16* w, int off) {
+  return unpack8(*reinterpret_cast<const uint4*>(w + off));
+}
+// cos, sin and -sin of 8 pairs
+__device__ __forceinline__ void load_turn(const float2* table, size_t off, Oct& c, Oct& s, Oct& ns) {
   const float4* tp = reinterpret_cast<const float4*>(table + off);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float4 v = tp[j];
-    c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
+    c.v[j] = f2_pack(v.x, v.z);
+    s.v[j] = f2_pack(v.y, v.w);
+    ns.v[j] = f2_pack(-v.y, -v.w);
   }
 }
+__device__ __forceinline__ float f2_sum(uint64_t v) { return f2_lo(v) + f2_hi(v); }
 
 // Sum over the CH (4 or 8) lanes of a row; all 32 lanes of the warp take part.
 template <int CH>
@@ -66,29 +73,38 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(mean(x^2) + eps) of a row, this lane holding x1 and x2
+template <int D>
+__device__ __forceinline__ float row_rms(const Oct& x1, const Oct& x2, float eps) {
+  uint64_t sa = f2_mul(x1.v[0], x1.v[0]), sb = f2_mul(x2.v[0], x2.v[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) {
+    sa = f2_fma(x1.v[j], x1.v[j], sa);
+    sb = f2_fma(x2.v[j], x2.v[j], sb);
+  }
+  return rsqrtf(row_sum<D / 16>(f2_sum(f2_add(sa, sb))) * (1.f / D) + eps);
+}
+
 // y = R(a) (r x w) of one lane's two octets; NORM false: r x w = x.
 template <int D, bool NORM>
-__device__ __forceinline__ void norm_rope_row(const uint4& u1, const uint4& u2, const float (&w1)[8],
-                                              const float (&w2)[8], const float (&c)[8], const float (&s)[8],
-                                              float eps, uint4& o1, uint4& o2) {
-  float x1[8], x2[8], y1[8], y2[8];
-  unpack8(u1, x1);
-  unpack8(u2, x2);
+__device__ __forceinline__ void norm_rope_row(const uint4& u1, const uint4& u2, const Oct& w1, const Oct& w2,
+                                              const Oct& c, const Oct& s, const Oct& ns, float eps, uint4& o1,
+                                              uint4& o2) {
+  Oct x1 = unpack8(u1), x2 = unpack8(u2);
   if (NORM) {
-    float ss = 0.f;
+    const float r = row_rms<D>(x1, x2, eps);
+    const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x1[j], x1[j], fmaf(x2[j], x2[j], ss));
-    const float r = rsqrtf(row_sum<D / 16>(ss) * (1.f / D) + eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x1[j] *= r * w1[j];
-      x2[j] *= r * w2[j];
+    for (int j = 0; j < 4; ++j) {
+      x1.v[j] = f2_mul(x1.v[j], f2_mul(r2, w1.v[j]));
+      x2.v[j] = f2_mul(x2.v[j], f2_mul(r2, w2.v[j]));
     }
   }
+  Oct y1, y2;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y1[j] = fmaf(x1[j], c[j], -x2[j] * s[j]);
-    y2[j] = fmaf(x1[j], s[j], x2[j] * c[j]);
+  for (int j = 0; j < 4; ++j) {
+    y1.v[j] = f2_fma(x2.v[j], ns.v[j], f2_mul(x1.v[j], c.v[j]));
+    y2.v[j] = f2_fma(x1.v[j], s.v[j], f2_mul(x2.v[j], c.v[j]));
   }
   o1 = pack8(y1);
   o2 = pack8(y2);
@@ -121,15 +137,14 @@ __global__ void __launch_bounds__(256) s2_qknorm_fwd_kernel(QkNormArgs a) {
         u2[k] = *reinterpret_cast<const uint4*>(src + k * D + D / 2);
       }
     }
-    float c[8], s[8], w1[8], w2[8];
-    load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s);
+    Oct c, s, ns;
+    load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s, ns);
     const W* w = static_cast<const W*>(is_q ? a.wq : a.wk);
-    load_w8(w, ch * 8, w1);
-    load_w8(w, ch * 8 + D / 2, w2);
+    const Oct w1 = load_w8(w, ch * 8), w2 = load_w8(w, ch * 8 + D / 2);
 #pragma unroll
     for (int k = 0; k < HG; ++k) {
       uint4 o1, o2;
-      norm_rope_row<D, true>(u1[k], u2[k], w1, w2, c, s, a.eps, o1, o2);
+      norm_rope_row<D, true>(u1[k], u2[k], w1, w2, c, s, ns, a.eps, o1, o2);
       if (live && h0 + k < heads) {
         *reinterpret_cast<uint4*>(dst + k * D) = o1;
         *reinterpret_cast<uint4*>(dst + k * D + D / 2) = o2;
@@ -153,11 +168,8 @@ __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
     const __nv_bfloat16* dy = which ? a.gk : a.gq;
     __nv_bfloat16* dx = which ? a.yk : a.yq;
     const W* w = static_cast<const W*>(which ? a.wk : a.wq);
-    float w1[8], w2[8], acc1[8], acc2[8];
-    load_w8(w, ch * 8, w1);
-    load_w8(w, ch * 8 + D / 2, w2);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc1[j] = acc2[j] = 0.f;
+    const Oct w1 = load_w8(w, ch * 8), w2 = load_w8(w, ch * 8 + D / 2);
+    Oct acc1 = {{0ull, 0ull, 0ull, 0ull}}, acc2 = acc1;
     const int G = (heads + HG - 1) / HG;
     const long long n = static_cast<long long>(a.tokens) * G * CH;
     for (long long e0 = blockIdx.x * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += gridDim.x * 256LL) {
@@ -177,34 +189,32 @@ __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
           d2[k] = *reinterpret_cast<const uint4*>(dy + off + k * D + D / 2);
         }
       }
-      float c[8], s[8];
-      load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s);
+      Oct c, s, ns;
+      load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s, ns);
 #pragma unroll
       for (int k = 0; k < HG; ++k) {
-        float x1[8], x2[8], g1[8], g2[8];
-        unpack8(u1[k], x1);
-        unpack8(u2[k], x2);
-        unpack8(d1[k], g1);
-        unpack8(d2[k], g2);
-        float ss = 0.f;
+        const Oct x1 = unpack8(u1[k]), x2 = unpack8(u2[k]);
+        Oct g1 = unpack8(d1[k]), g2 = unpack8(d2[k]);
+        const float r = row_rms<D>(x1, x2, a.eps);
+        const uint64_t r2 = f2_pack(r, r);
+        uint64_t sa = 0ull, sb = 0ull;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x1[j], x1[j], fmaf(x2[j], x2[j], ss));
-        const float r = rsqrtf(row_sum<CH>(ss) * (1.f / D) + a.eps);
-        float gx = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {  // du, then dw += du r x, g = du w, sum of g x
-          const float du1 = fmaf(g1[j], c[j], g2[j] * s[j]), du2 = fmaf(g2[j], c[j], -g1[j] * s[j]);
-          acc1[j] = fmaf(du1, r * x1[j], acc1[j]);
-          acc2[j] = fmaf(du2, r * x2[j], acc2[j]);
-          g1[j] = du1 * w1[j];
-          g2[j] = du2 * w2[j];
-          gx = fmaf(g1[j], x1[j], fmaf(g2[j], x2[j], gx));
+        for (int j = 0; j < 4; ++j) {  // du, then dw += du r x, g = du w, sum of g x
+          const uint64_t du1 = f2_fma(g2.v[j], s.v[j], f2_mul(g1.v[j], c.v[j]));
+          const uint64_t du2 = f2_fma(g1.v[j], ns.v[j], f2_mul(g2.v[j], c.v[j]));
+          acc1.v[j] = f2_fma(du1, f2_mul(r2, x1.v[j]), acc1.v[j]);
+          acc2.v[j] = f2_fma(du2, f2_mul(r2, x2.v[j]), acc2.v[j]);
+          g1.v[j] = f2_mul(du1, w1.v[j]);
+          g2.v[j] = f2_mul(du2, w2.v[j]);
+          sa = f2_fma(g1.v[j], x1.v[j], sa);
+          sb = f2_fma(g2.v[j], x2.v[j], sb);
         }
-        const float m = row_sum<CH>(gx) * (1.f / D) * r * r;
+        const float nm = row_sum<CH>(f2_sum(f2_add(sa, sb))) * (-1.f / D) * r * r * r;
+        const uint64_t nm2 = f2_pack(nm, nm);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          g1[j] = r * fmaf(-m, x1[j], g1[j]);
-          g2[j] = r * fmaf(-m, x2[j], g2[j]);
+        for (int j = 0; j < 4; ++j) {  // dx = r g - r^3 mean(g x) x
+          g1.v[j] = f2_fma(x1.v[j], nm2, f2_mul(r2, g1.v[j]));
+          g2.v[j] = f2_fma(x2.v[j], nm2, f2_mul(r2, g2.v[j]));
         }
         if (live && h0 + k < heads) {
           *reinterpret_cast<uint4*>(dx + off + k * D) = pack8(g1);
@@ -213,19 +223,21 @@ __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {  // lanes of equal chunk, then the block's warps
+    for (int j = 0; j < 4; ++j) {  // lanes of equal chunk, then the block's warps
 #pragma unroll
       for (int m = CH; m < 32; m <<= 1) {
-        acc1[j] += __shfl_xor_sync(0xffffffffu, acc1[j], m);
-        acc2[j] += __shfl_xor_sync(0xffffffffu, acc2[j], m);
+        acc1.v[j] = f2_add(acc1.v[j], __shfl_xor_sync(0xffffffffu, acc1.v[j], m));
+        acc2.v[j] = f2_add(acc2.v[j], __shfl_xor_sync(0xffffffffu, acc2.v[j], m));
       }
     }
     __syncthreads();  // red[] of the query pass has been read
     if (lane < CH) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        red[warp][ch * 8 + j] = acc1[j];
-        red[warp][ch * 8 + D / 2 + j] = acc2[j];
+      for (int j = 0; j < 4; ++j) {
+        red[warp][ch * 8 + 2 * j] = f2_lo(acc1.v[j]);
+        red[warp][ch * 8 + 2 * j + 1] = f2_hi(acc1.v[j]);
+        red[warp][ch * 8 + D / 2 + 2 * j] = f2_lo(acc2.v[j]);
+        red[warp][ch * 8 + D / 2 + 2 * j + 1] = f2_hi(acc2.v[j]);
       }
     }
     __syncthreads();
@@ -293,17 +305,17 @@ __global__ void __launch_bounds__(256) s2_cache_append_kernel(CacheAppendArgs a)
         u2[k] = *reinterpret_cast<const uint4*>(src + k * D + D / 2);
       }
     }
-    float c[8], s[8], w1[8], w2[8];
-    load_turn(a.table, static_cast<size_t>(live ? pos : 0) * (D / 2) + ch * 8, c, s);
+    Oct c, s, ns, w1 = {}, w2 = {};
+    load_turn(a.table, static_cast<size_t>(live ? pos : 0) * (D / 2) + ch * 8, c, s, ns);
     if (NORM) {
       const W* w = static_cast<const W*>(kind == 0 ? a.wq : a.wk);
-      load_w8(w, ch * 8, w1);
-      load_w8(w, ch * 8 + D / 2, w2);
+      w1 = load_w8(w, ch * 8);
+      w2 = load_w8(w, ch * 8 + D / 2);
     }
 #pragma unroll
     for (int k = 0; k < HG; ++k) {
       uint4 o1, o2;
-      norm_rope_row<D, NORM>(u1[k], u2[k], w1, w2, c, s, a.eps, o1, o2);
+      norm_rope_row<D, NORM>(u1[k], u2[k], w1, w2, c, s, ns, a.eps, o1, o2);
       if (live && h0 + k < heads) {
         *reinterpret_cast<uint4*>(dst + k * D) = kind == 2 ? u1[k] : o1;
         *reinterpret_cast<uint4*>(dst + k * D + D / 2) = kind == 2 ? u2[k] : o2;
