@@ -25,9 +25,9 @@ def _stream(device=None) -> int:
 
 def _need(name: str, t: torch.Tensor, shape, dtype=torch.bfloat16, device=None) -> None:
     try:  # the usual case in as few steps as it takes; what fails is named below
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            if t.is_cuda if device is None else t.device == device:
-                return
+        if (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+                and (device is None or t.device == device)):
+            return
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor):
@@ -565,7 +565,11 @@ def _workspace(fn: str, workspace, need: int, dev):
 
 class QKNormRope(torch.autograd.Function):
     """Autograd wrapper of the query/key norm with rotation: gradients for q,
-    k and both norm weights."""
+    k and both norm weights (once: the gradient itself has none).  To capture a
+    training step into a CUDA graph, call qknorm_rope_forward / _backward, or
+    capture with torch.autograd.grad while no eager graph of the same leaves is
+    alive: a leaf's gradient accumulation stays on the stream that first used
+    it."""
 
     @staticmethod
     def forward(ctx, q, k, w_q, w_k, table, eps=1e-6):
@@ -575,6 +579,7 @@ class QKNormRope(torch.autograd.Function):
         return q_out, k_out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, w_q, w_k, table = ctx.saved_tensors
         dq, dk, dw_q, dw_k = qknorm_rope_backward(q, k, w_q, w_k, dq_out.contiguous(), dk_out.contiguous(), table,

@@ -28,13 +28,45 @@ namespace s2 {
 
 namespace {
 
-// An octet of values as 4 packed pairs: the arithmetic runs on pairs
-// (fma.rn.f32x2), which halves its instructions; on single floats the backward
-// filled half of the issue slots and reached 66% of the DRAM's cycles.
+// 8 weights of one half at w + off, as fp32.
+__device__ __forceinline__ void load_w8(const float* w, int off, float (&o)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(w + off), b = *reinterpret_cast<const float4*>(w + off + 4);
+  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float (&o)[8]) {
+  const uint32_t p[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&p[j]));
+    o[2 * j] = f.x;
+    o[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void load_w8(const __nv_bfloat16* w, int off, float (&o)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(w + off), o);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void load_turn(const float2* table, size_t off, float (&c)[8], float (&s)[8]) {
+  const float4* tp = reinterpret_cast<const float4*>(table + off);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = tp[j];
+    c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
+  }
+}
+
+// The backward's octets as 4 packed pairs: its arithmetic runs on pairs
+// (fma.rn.f32x2), which halves its instructions (297 us at 32768 tokens x 72
+// heads of 128, 318 on single floats, which filled half of the issue slots).
+// The forward, with less arithmetic a byte, is faster on single floats (58 us at
+// 16384 x 40 heads, 61 on pairs; the appended prompts of 16K tokens 130 and 138).
 struct Oct {
   uint64_t v[4];
 };
-__device__ __forceinline__ Oct unpack8(const uint4& u) {
+__device__ __forceinline__ Oct unpack_oct(const uint4& u) {
   const uint32_t p[4] = {u.x, u.y, u.z, u.w};
   Oct o;
 #pragma unroll
@@ -45,15 +77,15 @@ __device__ __forceinline__ uint4 pack8(const Oct& f) {
   return make_uint4(f2_to_bf16x2(f.v[0]), f2_to_bf16x2(f.v[1]), f2_to_bf16x2(f.v[2]), f2_to_bf16x2(f.v[3]));
 }
 // 8 weights of one half at w + off, as fp32.
-__device__ __forceinline__ Oct load_w8(const float* w, int off) {
+__device__ __forceinline__ Oct load_oct(const float* w, int off) {
   const float4 a = *reinterpret_cast<const float4*>(w + off), b = *reinterpret_cast<const float4*>(w + off + 4);
   return {{f2_pack(a.x, a.y), f2_pack(a.z, a.w), f2_pack(b.x, b.y), f2_pack(b.z, b.w)}};
 }
-__device__ __forceinline__ Oct load_w8(const __nv_bfloat16* w, int off) {
-  return unpack8(*reinterpret_cast<const uint4*>(w + off));
+__device__ __forceinline__ Oct load_oct(const __nv_bfloat16* w, int off) {
+  return unpack_oct(*reinterpret_cast<const uint4*>(w + off));
 }
 // cos, sin and -sin of 8 pairs
-__device__ __forceinline__ void load_turn(const float2* table, size_t off, Oct& c, Oct& s, Oct& ns) {
+__device__ __forceinline__ void load_turn_oct(const float2* table, size_t off, Oct& c, Oct& s, Oct& ns) {
   const float4* tp = reinterpret_cast<const float4*>(table + off);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -87,24 +119,27 @@ __device__ __forceinline__ float row_rms(const Oct& x1, const Oct& x2, float eps
 
 // y = R(a) (r x w) of one lane's two octets; NORM false: r x w = x.
 template <int D, bool NORM>
-__device__ __forceinline__ void norm_rope_row(const uint4& u1, const uint4& u2, const Oct& w1, const Oct& w2,
-                                              const Oct& c, const Oct& s, const Oct& ns, float eps, uint4& o1,
-                                              uint4& o2) {
-  Oct x1 = unpack8(u1), x2 = unpack8(u2);
+__device__ __forceinline__ void norm_rope_row(const uint4& u1, const uint4& u2, const float (&w1)[8],
+                                              const float (&w2)[8], const float (&c)[8], const float (&s)[8],
+                                              float eps, uint4& o1, uint4& o2) {
+  float x1[8], x2[8], y1[8], y2[8];
+  unpack8(u1, x1);
+  unpack8(u2, x2);
   if (NORM) {
-    const float r = row_rms<D>(x1, x2, eps);
-    const uint64_t r2 = f2_pack(r, r);
+    float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x1.v[j] = f2_mul(x1.v[j], f2_mul(r2, w1.v[j]));
-      x2.v[j] = f2_mul(x2.v[j], f2_mul(r2, w2.v[j]));
+    for (int j = 0; j < 8; ++j) ss = fmaf(x1[j], x1[j], fmaf(x2[j], x2[j], ss));
+    const float r = rsqrtf(row_sum<D / 16>(ss) * (1.f / D) + eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x1[j] *= r * w1[j];
+      x2[j] *= r * w2[j];
     }
   }
-  Oct y1, y2;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    y1.v[j] = f2_fma(x2.v[j], ns.v[j], f2_mul(x1.v[j], c.v[j]));
-    y2.v[j] = f2_fma(x1.v[j], s.v[j], f2_mul(x2.v[j], c.v[j]));
+  for (int j = 0; j < 8; ++j) {
+    y1[j] = fmaf(x1[j], c[j], -x2[j] * s[j]);
+    y2[j] = fmaf(x1[j], s[j], x2[j] * c[j]);
   }
   o1 = pack8(y1);
   o2 = pack8(y2);
@@ -137,14 +172,15 @@ __global__ void __launch_bounds__(256) s2_qknorm_fwd_kernel(QkNormArgs a) {
         u2[k] = *reinterpret_cast<const uint4*>(src + k * D + D / 2);
       }
     }
-    Oct c, s, ns;
-    load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s, ns);
+    float c[8], s[8], w1[8], w2[8];
+    load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s);
     const W* w = static_cast<const W*>(is_q ? a.wq : a.wk);
-    const Oct w1 = load_w8(w, ch * 8), w2 = load_w8(w, ch * 8 + D / 2);
+    load_w8(w, ch * 8, w1);
+    load_w8(w, ch * 8 + D / 2, w2);
 #pragma unroll
     for (int k = 0; k < HG; ++k) {
       uint4 o1, o2;
-      norm_rope_row<D, true>(u1[k], u2[k], w1, w2, c, s, ns, a.eps, o1, o2);
+      norm_rope_row<D, true>(u1[k], u2[k], w1, w2, c, s, a.eps, o1, o2);
       if (live && h0 + k < heads) {
         *reinterpret_cast<uint4*>(dst + k * D) = o1;
         *reinterpret_cast<uint4*>(dst + k * D + D / 2) = o2;
@@ -168,7 +204,7 @@ __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
     const __nv_bfloat16* dy = which ? a.gk : a.gq;
     __nv_bfloat16* dx = which ? a.yk : a.yq;
     const W* w = static_cast<const W*>(which ? a.wk : a.wq);
-    const Oct w1 = load_w8(w, ch * 8), w2 = load_w8(w, ch * 8 + D / 2);
+    const Oct w1 = load_oct(w, ch * 8), w2 = load_oct(w, ch * 8 + D / 2);
     Oct acc1 = {{0ull, 0ull, 0ull, 0ull}}, acc2 = acc1;
     const int G = (heads + HG - 1) / HG;
     const long long n = static_cast<long long>(a.tokens) * G * CH;
@@ -190,11 +226,11 @@ __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
         }
       }
       Oct c, s, ns;
-      load_turn(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s, ns);
+      load_turn_oct(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s, ns);
 #pragma unroll
       for (int k = 0; k < HG; ++k) {
-        const Oct x1 = unpack8(u1[k]), x2 = unpack8(u2[k]);
-        Oct g1 = unpack8(d1[k]), g2 = unpack8(d2[k]);
+        const Oct x1 = unpack_oct(u1[k]), x2 = unpack_oct(u2[k]);
+        Oct g1 = unpack_oct(d1[k]), g2 = unpack_oct(d2[k]);
         const float r = row_rms<D>(x1, x2, a.eps);
         const uint64_t r2 = f2_pack(r, r);
         uint64_t sa = 0ull, sb = 0ull;
@@ -305,17 +341,17 @@ __global__ void __launch_bounds__(256) s2_cache_append_kernel(CacheAppendArgs a)
         u2[k] = *reinterpret_cast<const uint4*>(src + k * D + D / 2);
       }
     }
-    Oct c, s, ns, w1 = {}, w2 = {};
-    load_turn(a.table, static_cast<size_t>(live ? pos : 0) * (D / 2) + ch * 8, c, s, ns);
+    float c[8], s[8], w1[8], w2[8];
+    load_turn(a.table, static_cast<size_t>(live ? pos : 0) * (D / 2) + ch * 8, c, s);
     if (NORM) {
       const W* w = static_cast<const W*>(kind == 0 ? a.wq : a.wk);
-      w1 = load_w8(w, ch * 8);
-      w2 = load_w8(w, ch * 8 + D / 2);
+      load_w8(w, ch * 8, w1);
+      load_w8(w, ch * 8 + D / 2, w2);
     }
 #pragma unroll
     for (int k = 0; k < HG; ++k) {
       uint4 o1, o2;
-      norm_rope_row<D, NORM>(u1[k], u2[k], w1, w2, c, s, ns, a.eps, o1, o2);
+      norm_rope_row<D, NORM>(u1[k], u2[k], w1, w2, c, s, a.eps, o1, o2);
       if (live && h0 + k < heads) {
         *reinterpret_cast<uint4*>(dst + k * D) = kind == 2 ? u1[k] : o1;
         *reinterpret_cast<uint4*>(dst + k * D + D / 2) = kind == 2 ? u2[k] : o2;

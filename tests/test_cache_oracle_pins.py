@@ -139,3 +139,7 @@ def test_python_calls_refuse_host_tensors_and_wrong_shapes():
         s2.cache_attention(x, x, x, i, i, i)
     with pytest.raises(ValueError, match=r"\[T, H, D\]"):
         s2.cache_append(x, x, x, tab, i, i, x, x)
+    with pytest.raises(ValueError, match="CUDA"):  # the first operand names the device of the others
+        s2.nf4_dequantize(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, dtype=torch.int8), torch.zeros(1))
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        s2.api._need("x", 5, (1,))

@@ -194,6 +194,13 @@ def test_chain_attention_against_oracle(kernel, lens, H, Hkv, D, bs):
     assert (o[t:] == 5.0).all() and (l[:, t:] == 9.0).all()  # rows of no request as they were
 
 
+@pytest.mark.parametrize("H,Hkv,D,bs", [(40, 1, 64, 16), (128, 1, 128, 64)])
+@pytest.mark.parametrize("lens", ["one", "tile-edges", "ragged", "gaps"])
+def test_more_than_16_heads_a_kv_head(lens, H, Hkv, D, bs):
+    b = _batch(LENS[lens], H, Hkv, D, bs, None, 8)
+    _check(b, *_call(b))
+
+
 @pytest.mark.parametrize("H,Hkv,D,bs", [(4, 4, 128, 16), (32, 4, 64, 128), (5, 1, 128, 64)])
 @pytest.mark.parametrize("lens,drop", [("drafts", 0.0), ("ragged", 0.0), ("drafts", 0.4), ("one", 1.0), ("tile-edges", 1.0)])
 def test_tree_attention_against_oracle(kernel, lens, drop, H, Hkv, D, bs):
@@ -405,3 +412,54 @@ def test_captured_step_follows_new_lengths(kernel):
         torch.cuda.synchronize()
         assert torch.equal(cap[0], want[0]) and torch.equal(cap[1], want[1]) and torch.equal(kg, ke)
     assert s2().device_status() == 0
+
+
+def test_two_streams_at_once_and_refusals():
+    b = _batch([(900, 3), (77, 1), (0, 9), (4000, 2)], 16, 4, 128, 64, None, 21)
+    args = [b["q"].cuda(), b["kc"].cuda(), b["vc"].cuda(), i32(b["tab"]), i32([c for c, _ in b["lens"]]), i32(b["cu"])]
+    want = s2().cache_attention(*args)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(3)], []
+    for st in streams * 4:
+        with torch.cuda.stream(st):
+            got.append(s2().cache_attention(*args))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in got)
+    f = s2().cache_attention
+    with pytest.raises(ValueError, match="v_cache"):
+        f(args[0], args[1], args[2][:-1], *args[3:])
+    with pytest.raises(ValueError, match="contiguous"):
+        f(args[0], args[1].transpose(1, 2).contiguous().transpose(1, 2), *args[2:])
+    with pytest.raises(ValueError, match="int32"):
+        f(*args[:3], args[3].long(), *args[4:])
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        f(*args[:5], args[5][:-1])
+    with pytest.raises(ValueError, match="mask"):
+        f(*args, mask=torch.zeros(3, dtype=torch.int64, device="cuda"))
+    with pytest.raises(s2().S2AttnError, match="WORKSPACE"):
+        f(*args, workspace=torch.zeros(64, device="cuda"))
+    with pytest.raises(s2().S2AttnError, match="UNSUPPORTED"):
+        f(args[0], args[1].view(-1, 8, 4, 128), args[2].view(-1, 8, 4, 128), *args[3:])
+    with pytest.raises(s2().S2AttnError, match="INVALID"):
+        f(args[0][:0].contiguous(), *args[1:])
+    with pytest.raises(s2().S2AttnError, match="INVALID"):
+        s2().cache_plan(args[4], args[4], args[3], i32([1]), 16, 0)
+
+
+def test_projection_to_attention_decodes_a_prompt():
+    """NF4 projection, plan, append and attention of a prompt in one step agree
+    with projection, rotation and dense attention."""
+    H, Hkv, D, K, N = 4, 2, 64, 256, 128
+    codes, sq, c2 = (t.cuda() for t in I.make_nf4_weights((H + 2 * Hkv) * D, K, seed=2))
+    x = I.randn_bf16((1, N, K), 30).cuda()
+    q, k, v = s2().nf4_qkv(x, codes, sq, c2, H, Hkv, D)
+    tab = s2().rope_table(N, D, 1.0)
+    dense = s2().dense_causal_attn(s2().rope_apply(q, tab), s2().rope_apply(k, tab), v)[0]
+    blocks = torch.full((1, 8), -1, dtype=torch.int32, device="cuda")
+    p = s2().cache_plan(i32([0]), i32([N]), blocks, torch.randperm(8, device="cuda").int(), 16, N)
+    kc = torch.empty(8, 16, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    qr = s2().cache_append(q[0], k[0], v[0], tab, p.positions, p.slots, kc, vc)
+    o, _ = s2().cache_attention(qr, kc, vc, blocks, i32([0]), p.cu_seqlens)
+    a, b = to64(o), to64(dense)
+    assert np.all(np.abs(a - b) <= 2 * 2.0 ** -8 * np.abs(b) + 2 * (2.0 ** -8 + 2.0 ** -12) * np.abs(to64(v)).max())

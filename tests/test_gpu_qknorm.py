@@ -199,3 +199,53 @@ def test_other_stream_and_captured_graph():
         g.replay()
         ref = (*s2().qknorm_rope_forward(x, k, wq, wk, tab), *s2().qknorm_rope_backward(x, k, wq, wk, gq, gk, tab))
         assert all(torch.equal(a, b) for a, b in zip(ref, cap))
+
+
+def test_autograd_captured_with_its_gradients():
+    B, N, H, Hkv, D, G = 1, 512, 4, 2, 64, 256
+    q, k, wq, wk, do, _ = (t.cuda() for t in _case(B, N, H, Hkv, D, torch.float32, seed=90))
+    v = I.randn_bf16((B, N, Hkv, D), 95).cuda()
+    tab = s2().rope_table(N, D, 1.0)
+
+    def step():
+        leaves = [t.detach().requires_grad_() for t in (q, k, v, wq, wk)]
+        o = s2().s2_qknorm_attn(*leaves, G, tab)
+        return (o.detach(), *torch.autograd.grad(o, leaves, do))
+
+    want = step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_python_refusals_on_the_gpu():
+    q, k, wq, wk, gq, gk = (t.cuda() for t in _case(1, 32, 4, 2, 64, torch.float32))
+    tab = s2().rope_table(32, 64, 1.0)
+    f = s2().qknorm_rope_forward
+    with pytest.raises(ValueError, match="contiguous"):
+        f(q.transpose(1, 2).contiguous().transpose(1, 2), k, wq, wk, tab)
+    with pytest.raises(ValueError, match="bfloat16"):
+        f(q.float(), k, wq, wk, tab)
+    with pytest.raises(ValueError, match="w_q"):
+        f(q, k, wq.half(), wk, tab)
+    with pytest.raises(ValueError, match="w_k"):
+        f(q, k, wq, wk.bfloat16(), tab)
+    with pytest.raises(ValueError, match="table"):
+        f(q, k, wq, wk, tab[:16])
+    with pytest.raises(ValueError, match="expected cuda"):
+        s2().api._need("k", torch.zeros(1, device="cuda"), (1,), torch.float32, torch.device("cuda", 1))
+    with pytest.raises(s2().S2AttnError, match="INVALID"):
+        f(q, k, wq, wk, tab, eps=0.0)
+    with pytest.raises(s2().S2AttnError, match="WORKSPACE"):
+        s2().qknorm_rope_backward(q, k, wq, wk, gq, gk, tab, workspace=torch.zeros(16, device="cuda"))
+    with pytest.raises(ValueError, match="dq has shape"):
+        s2().qknorm_rope_backward(q, k, wq, wk, gq, gk, tab, dq=gk)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        x = q.detach().requires_grad_()
+        y, _ = s2().QKNormRope.apply(x, k, wq, wk, tab)
+        g, = torch.autograd.grad(y, x, gq.detach().requires_grad_(), create_graph=True)
+        g.sum().backward()
