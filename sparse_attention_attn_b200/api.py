@@ -472,7 +472,7 @@ def _run(dev, fn: str, *args) -> None:
     """One C call with `dev` current, on its current stream.  The device guard
     is entered only where it changes something: the smallest calls take a few
     microseconds on the GPU, and the guard as long on the host."""
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = getattr(_lib.load(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -486,18 +486,12 @@ def _run(dev, fn: str, *args) -> None:
 def _need_norm_weights(w_q, w_k, D: int, dev) -> int:
     """Checks the two [D] norm weights; 1 for fp32, 0 for bf16."""
     dtype = getattr(w_q, "dtype", None)
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise ValueError(f"w_q must be a torch.float32 or torch.bfloat16 tensor, got {dtype}")
-    _need("w_q", w_q, (D,), dtype, device=dev)
-    _need("w_k", w_k, (D,), dtype, device=dev)
-    return int(dtype == torch.float32)
-
-
-def _need_table(table, D: int, dev, rows=None) -> int:
-    if not isinstance(table, torch.Tensor) or table.dim() != 3:
-        raise ValueError("table must be a [rows, D/2, 2] tensor (rope_table)")
-    _need("table", table, (table.shape[0] if rows is None else rows, D // 2, 2), torch.float32, device=dev)
-    return table.shape[0]
+    shape = (D,)
+    _need("w_q", w_q, shape, dtype, dev)
+    _need("w_k", w_k, shape, dtype, dev)
+    return 1 if dtype is torch.float32 else 0
 
 
 def qknorm_rope_forward(q, k, w_q, w_k, table, eps: float = 1e-6, q_out=None, k_out=None):
@@ -510,7 +504,7 @@ def qknorm_rope_forward(q, k, w_q, w_k, table, eps: float = 1e-6, q_out=None, k_
     dev = q.device
     _need("k", k, (B, N, Hkv, D), device=dev)
     w32 = _need_norm_weights(w_q, w_k, D, dev)
-    _need_table(table, D, dev, N)
+    _need("table", table, (N, D // 2, 2), torch.float32, dev)
     q_out = _out("q_out", q_out, q)
     k_out = _out("k_out", k_out, k)
     _run(dev, "s2attn_qknorm_rope_fwd", q.data_ptr(), k.data_ptr(), w_q.data_ptr(), w_k.data_ptr(), table.data_ptr(),
@@ -530,7 +524,7 @@ def qknorm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, table, eps: float = 1e-
     _need("dq_out", dq_out, (B, N, H, D), device=dev)
     _need("dk_out", dk_out, (B, N, Hkv, D), device=dev)
     w32 = _need_norm_weights(w_q, w_k, D, dev)
-    _need_table(table, D, dev, N)
+    _need("table", table, (N, D // 2, 2), torch.float32, dev)
     dq, dk = _out("dq", dq, q), _out("dk", dk, k)
     dw_q, dw_k = _out("dw_q", dw_q, w_q), _out("dw_k", dw_k, w_k)
     workspace, wsb = _workspace("s2attn_qknorm_rope_bwd", workspace, _lib.s2attn_qknorm_rope_bwd_workspace_bytes(D),
@@ -605,10 +599,6 @@ class CachePlan(NamedTuple):
     counts: torch.Tensor              # [4] blocks taken, needed, new tokens, tokens left without a block
 
 
-def _need_ints(name: str, t, shape, dev=None) -> None:
-    _need(name, t, shape, torch.int32, device=dev)
-
-
 def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, num_tokens: int, parents=None):
     """Blocks, slots and positions for the new tokens of a ragged batch, on the
     GPU.  ctx_lens, new_lens int32 [R]: tokens in the cache and tokens to add;
@@ -621,22 +611,22 @@ def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, n
     if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
         raise ValueError("ctx_lens must be an int32 tensor [R]")
     R, T = ctx_lens.shape[0], int(num_tokens)
-    _need_ints("ctx_lens", ctx_lens, (R,))
+    _need("ctx_lens", ctx_lens, (R,), torch.int32)
     dev = ctx_lens.device
-    _need_ints("new_lens", new_lens, (R,), dev)
+    _need("new_lens", new_lens, (R,), torch.int32, dev)
     if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
         raise ValueError("block_tables must be an int32 tensor [R, max_blocks]")
-    _need_ints("block_tables", block_tables, (R, block_tables.shape[1]), dev)
+    _need("block_tables", block_tables, (R, block_tables.shape[1]), torch.int32, dev)
     if not isinstance(free_blocks, torch.Tensor) or free_blocks.dim() != 1:
         raise ValueError("free_blocks must be an int32 tensor [num_free]")
-    _need_ints("free_blocks", free_blocks, (free_blocks.shape[0],), dev)
+    _need("free_blocks", free_blocks, (free_blocks.shape[0],), torch.int32, dev)
     if parents is not None:
-        _need_ints("parents", parents, (T,), dev)
+        _need("parents", parents, (T,), torch.int32, dev)
     if T <= 0:
         raise _lib.S2AttnError("s2attn_cache_plan", _lib.S2ATTN_ERR_INVALID_ARG)
     mask = None if parents is None else torch.empty(T, dtype=torch.int64, device=dev)
     buf = torch.empty(2 * T + R + 5, dtype=torch.int32, device=dev)  # one allocation
-    positions, slots, cu_seqlens, counts = buf.split((T, T, R + 1, 4))
+    positions, slots, cu_seqlens, counts = buf.split_with_sizes((T, T, R + 1, 4))
     p = buf.data_ptr()
     _run(dev, "s2attn_cache_plan", ctx_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
          free_blocks.data_ptr(), None if parents is None else parents.data_ptr(), p + 8 * T, p, p + 4 * T, None if
@@ -673,10 +663,13 @@ def cache_append(q, k, v, table, positions, slots, k_cache, v_cache, w_q=None, w
     dev = q.device
     _need("k", k, (T, Hkv, D), device=dev)
     _need("v", v, (T, Hkv, D), device=dev)
-    _need_ints("positions", positions, (T,), dev)
-    _need_ints("slots", slots, (T,), dev)
+    _need("positions", positions, (T,), torch.int32, dev)
+    _need("slots", slots, (T,), torch.int32, dev)
     nb, bs, _ = _need_cache(k_cache, v_cache, Hkv, D, dev)
-    rows = _need_table(table, D, dev)
+    if not isinstance(table, torch.Tensor) or table.dim() != 3:
+        raise ValueError("table must be a [rows, D/2, 2] tensor (rope_table)")
+    rows = table.shape[0]
+    _need("table", table, (rows, D // 2, 2), torch.float32, dev)
     if (w_q is None) != (w_k is None):
         raise ValueError("w_q and w_k go together")
     w32 = 0 if w_q is None else _need_norm_weights(w_q, w_k, D, dev)
@@ -707,9 +700,9 @@ def cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mas
     if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
         raise ValueError("block_tables must be an int32 tensor [R, max_blocks]")
     R, maxb = block_tables.shape
-    _need_ints("block_tables", block_tables, (R, maxb), dev)
-    _need_ints("ctx_lens", ctx_lens, (R,), dev)
-    _need_ints("cu_seqlens", cu_seqlens, (R + 1,), dev)
+    _need("block_tables", block_tables, (R, maxb), torch.int32, dev)
+    _need("ctx_lens", ctx_lens, (R,), torch.int32, dev)
+    _need("cu_seqlens", cu_seqlens, (R + 1,), torch.int32, dev)
     if mask is not None:
         _need("mask", mask, (T,), torch.int64, device=dev)
     out = _out("out", out, q)
