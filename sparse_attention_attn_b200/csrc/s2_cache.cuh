@@ -171,6 +171,101 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? neg_inf() : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+// acc (bit patterns, 32 columns from c0 of one row) out: o normalised, or the partial as it is.
+__device__ __forceinline__ void store_o32(__nv_bfloat16* o, float* part, bool whole, const uint32_t (&v)[32], float inv) {
+  if (whole) {
+    store_row32(o, v, inv);
+  } else {
+    uint4* p = reinterpret_cast<uint4*>(part);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) p[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  }
+}
+
+// Adds the infinite and NaN values of V in the segment's drafts to the stored
+// row (o, or its part) of a token that sees them; any weight turns such a value
+// into itself.  Out of line: such values are an error of the model's.
+template <int D>
+__device__ __noinline__ void add_odd(const CacheAttnArgs& a, const Seg& sg, int token, __nv_bfloat16* o, float* part) {
+  const int j_tok = token - sg.row0, last = min((sg.kt0 + sg.tiles) * kTile, sg.keys);
+  const unsigned long long see = a.mask != nullptr ? visible_drafts(a, sg, token) : 0ull;
+  for (int key = max(sg.kt0 * kTile, sg.ctx); key < last; ++key) {
+    const int d = key - sg.ctx, blk = a.block_tables[static_cast<size_t>(sg.ri) * a.max_blocks + (key >> a.bs_log2)];
+    if (a.mask != nullptr ? d >= 64 || !(see >> d & 1) : d > j_tok) continue;
+    if (blk < 0 || blk >= a.num_blocks) continue;
+    const size_t place = (static_cast<size_t>(blk) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1));
+    const __nv_bfloat16* src = a.v_cache + (place * a.Hkv + sg.kvh) * D;
+    for (int i = 0; i < D; ++i) {
+      const float x = __bfloat162float(src[i]);
+      if (isfinite(x)) continue;
+      if (sg.whole)
+        o[i] = __float2bfloat16(__bfloat162float(o[i]) + x);
+      else
+        part[i] += x;
+    }
+  }
+}
+
+// Makes a landed V tile (128-byte-swizzled 64-column slabs of kTile rows) safe
+// for the product; the 128 threads of a warpgroup call it, `row` 0 .. 127.  Rows
+// behind the last key (`valid` rows hold keys) within its 16-key step are zeroed:
+// stale cache rows may hold anything.  So are infinite and NaN values of the
+// tile's drafts (its last `drafts` keys), which a product would add as 0 V to
+// rows that do not see them; `odd` is set, and add_odd adds them to the rows that
+// do.
+template <int D>
+__device__ __forceinline__ void clean_v(uint32_t tile, int valid, int drafts, int row, uint32_t& odd) {
+  const int rows = drafts + (-valid & 15);
+  for (int e = row; e < rows * (D / 8); e += 128) {
+    const int r = valid - drafts + e / (D / 8), c = e % (D / 8);
+    const uint32_t at = tile + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (r < valid) {
+      w = lds_u4(at);
+      if (!nonfinite8(w)) continue;
+      odd = 1;
+      uint32_t* h = &w.x;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if ((h[x] & 0x7f80u) == 0x7f80u) h[x] &= 0xffff0000u;
+        if ((h[x] & 0x7f800000u) == 0x7f800000u) h[x] &= 0xffffu;
+      }
+    }
+    st_shared_v4(at, w.x, w.y, w.z, w.w);
+  }
+  fence_proxy_async_smem();
+}
+
+// Scores of one row against the 128 keys from key0: -inf where the row's token
+// (the j_tok-th new one of the request) does not see the key.
+__device__ __forceinline__ void mask_row128(const CacheAttnArgs& a, const Seg& s, int key0, int j_tok,
+                                            uint32_t (&sr)[4][32]) {
+  if (a.mask == nullptr) {
+    const int lim = min(s.ctx + j_tok, s.keys - 1) - key0;  // last visible column
+#pragma unroll
+    for (int c = 0; c < 128; ++c)
+      if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(neg_inf());
+  } else {
+    // visible columns as 4 words: cached keys, then the draft bits (of the request's rows)
+    const unsigned long long see = j_tok < s.tok + s.ntok ? visible_drafts(a, s, s.row0 + j_tok) : 0ull;
+    const int d0 = s.ctx - key0;  // column of draft 0 (below 0: drafts begin in an earlier tile)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int at = d0 - 32 * w;  // draft 0 relative to this word
+      uint32_t bits;
+      if (at >= 32)
+        bits = 0xffffffffu;
+      else if (at > 0)
+        bits = ((1u << at) - 1u) | static_cast<uint32_t>(see << at);
+      else
+        bits = at > -64 ? static_cast<uint32_t>(see >> -at) : 0u;
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (!(bits >> c & 1u)) sr[w][c] = __float_as_uint(neg_inf());
+    }
+  }
+}
+
 // A part in the workspace: ROWS x D sums, then ROWS maxima (log2 units) and
 // ROWS sums.  CTA c's slot 1 holds the part of the item that begins in it,
 // slot 0 the part of an item that began before.

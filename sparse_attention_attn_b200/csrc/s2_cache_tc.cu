@@ -63,41 +63,6 @@ struct TcCfg {
   static_assert(SMEM <= 232448 - 2048, "shared memory");
 };
 
-// acc (bit patterns, 32 columns from c0 of one row) out: o normalised, or the partial as it is.
-__device__ __forceinline__ void store_o32(__nv_bfloat16* o, float* part, bool whole, const uint32_t (&v)[32], float inv) {
-  if (whole) {
-    store_row32(o, v, inv);
-  } else {
-    uint4* p = reinterpret_cast<uint4*>(part);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) p[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-  }
-}
-
-// Adds the infinite and NaN values of V in the segment's drafts to the stored
-// row (o, or its part) of a token that sees them; any weight turns such a value
-// into itself.  Out of line: such values are an error of the model's.
-template <int D>
-__device__ __noinline__ void add_odd(const CacheAttnArgs& a, const Seg& sg, int token, __nv_bfloat16* o, float* part) {
-  const int j_tok = token - sg.row0, last = min((sg.kt0 + sg.tiles) * kTile, sg.keys);
-  const unsigned long long see = a.mask != nullptr ? visible_drafts(a, sg, token) : 0ull;
-  for (int key = max(sg.kt0 * kTile, sg.ctx); key < last; ++key) {
-    const int d = key - sg.ctx, blk = a.block_tables[static_cast<size_t>(sg.ri) * a.max_blocks + (key >> a.bs_log2)];
-    if (a.mask != nullptr ? d >= 64 || !(see >> d & 1) : d > j_tok) continue;
-    if (blk < 0 || blk >= a.num_blocks) continue;
-    const size_t place = (static_cast<size_t>(blk) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1));
-    const __nv_bfloat16* src = a.v_cache + (place * a.Hkv + sg.kvh) * D;
-    for (int i = 0; i < D; ++i) {
-      const float x = __bfloat162float(src[i]);
-      if (isfinite(x)) continue;
-      if (sg.whole)
-        o[i] = __float2bfloat16(__bfloat162float(o[i]) + x);
-      else
-        part[i] += x;
-    }
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     s2_cache_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -389,29 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int Lv = L - 2 * n + (alt ? 4 * j + 2 * wg : 2 * j) + 1;
             ok = warp_wait(smem_u32(&bar_full[Lv % NS]), (Lv / NS) & 1, wc, 133);
             if (!ok) break;
-            // Rows of V behind the last key, within its 16-key step, are zeroed.
-            // So are infinite and NaN values of drafts, which a product would
-            // add as 0 V to rows that do not see them: add_odd adds them to the
-            // rows that do.
-            const int rows = drafts + (-valid & 15);
-            for (int e = row; e < rows * (D / 8); e += 128) {
-              const int r = valid - drafts + e / (D / 8), c = e % (D / 8);
-              const uint32_t at = kv_addr(Lv % NS) + (c >> 3) * C::ATOM + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-              uint4 w = make_uint4(0u, 0u, 0u, 0u);
-              if (r < valid) {
-                w = lds_u4(at);
-                if (!nonfinite8(w)) continue;
-                odd[ng % C::NG] = 1;
-                uint32_t* h = &w.x;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  if ((h[x] & 0x7f80u) == 0x7f80u) h[x] &= 0xffff0000u;
-                  if ((h[x] & 0x7f800000u) == 0x7f800000u) h[x] &= 0xffffu;
-                }
-              }
-              st_shared_v4(at, w.x, w.y, w.z, w.w);
-            }
-            fence_proxy_async_smem();
+            clean_v<D>(kv_addr(Lv % NS), valid, drafts, row, odd[ng % C::NG]);
           }
         }
         if (!busy) {  // no live row: only the protocol
@@ -428,31 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         if (edge) {
           // (the row's token is worked out here, for the one or two such tiles of a segment)
-          const int j_tok = sg.tok + (alt || wg == 0 ? 0 : a.tpt) + row / a.rep;
-          if (a.mask == nullptr) {
-            const int lim = min(ctx + j_tok, sg.keys - 1) - key0;  // last visible column
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(neg_inf());
-          } else {
-            // visible columns as 4 words: cached keys, then the draft bits (of the request's rows)
-            const unsigned long long see = j_tok < sg.tok + sg.ntok ? visible_drafts(a, sg, sg.row0 + j_tok) : 0ull;
-            const int d0 = ctx - key0;  // column of draft 0 (below 0: drafts begin in an earlier tile)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int at = d0 - 32 * w;  // draft 0 relative to this word
-              uint32_t bits;
-              if (at >= 32)
-                bits = 0xffffffffu;
-              else if (at > 0)
-                bits = ((1u << at) - 1u) | static_cast<uint32_t>(see << at);
-              else
-                bits = at > -64 ? static_cast<uint32_t>(see >> -at) : 0u;
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(bits >> c & 1u)) sr[w][c] = __float_as_uint(neg_inf());
-            }
-          }
+          mask_row128(a, sg, key0, sg.tok + (alt || wg == 0 ? 0 : a.tpt) + row / a.rep, sr);
         }
         float m4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
