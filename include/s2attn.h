@@ -411,8 +411,9 @@ S2ATTN_API size_t s2attn_cache_attn_workspace_bytes(int D);
  * and lse = -inf.  Rows of no request (behind cu_seqlens[R]) are left as they
  * were.  Scale 1/sqrt(D); kv head of query head h is h / (H / Hkv).
  * Keys in a block outside [0, num_blocks) count as zero vectors (and are
- * recorded); places behind a row of block_tables do not exist.
- * D in {64, 128}; block_size a power of two from 16 to 256; T H <= 2^30;
+ * recorded); places behind a row of block_tables do not exist.  Infinite and NaN
+ * values of a new token's key or value reach only the rows that see it.
+ * D in {64, 128}; H / Hkv <= 128; block_size a power of two from 16 to 256; T H <= 2^30;
  * num_blocks * block_size below 2^31, max_blocks * block_size at most 2^31 - 65536.
  * workspace: 16-byte aligned, s2attn_cache_attn_workspace_bytes(D) bytes, need
  * not be cleared; calls that overlap need one each.  Two launches; the result

@@ -107,7 +107,7 @@ INVALID, UNSUP, MISAL, WS = (_lib.S2ATTN_ERR_INVALID_ARG, _lib.S2ATTN_ERR_UNSUPP
     (plan, dict(par=P, mask=P + 4), MISAL),
     (attn, dict(p=None), INVALID), (attn, dict(T=0), INVALID), (attn, dict(R=0), INVALID), (attn, dict(maxb=0), INVALID),
     (attn, dict(H=4, Hkv=3), INVALID), (attn, dict(D=96), UNSUP), (attn, dict(bs=8), UNSUP), (attn, dict(bs=48), UNSUP),
-    (attn, dict(bs=512), UNSUP), (attn, dict(nb=1 << 28, bs=16), UNSUP), (attn, dict(T=1 << 29), UNSUP),
+    (attn, dict(bs=512), UNSUP), (attn, dict(H=258, Hkv=2), UNSUP), (attn, dict(nb=1 << 28, bs=16), UNSUP), (attn, dict(T=1 << 29), UNSUP),
     (attn, dict(p=P + 8), MISAL), (attn, dict(tab=P + 1), MISAL), (attn, dict(mask=P + 4), MISAL),
     (attn, dict(ws=None), WS), (attn, dict(wsb=100), WS), (attn, dict(ws=P + 8), WS),
 ])
