@@ -7,6 +7,7 @@ the device is not a B200, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -230,6 +231,7 @@ def s2attn_qknorm_rope_fwd(q, k, w_q, w_k, table, q_out, k_out, B, N, H, Hkv, D,
     return load().s2attn_qknorm_rope_fwd(q, k, w_q, w_k, table, q_out, k_out, B, N, H, Hkv, D, w_fp32, eps, stream)
 
 
+@functools.lru_cache(maxsize=None)  # a constant of the head dim
 def s2attn_qknorm_rope_bwd_workspace_bytes(D) -> int:
     return load().s2attn_qknorm_rope_bwd_workspace_bytes(D)
 
@@ -252,6 +254,7 @@ def s2attn_cache_append(q, k, v, w_q, w_k, table, positions, slots, q_out, k_cac
                                       D, table_rows, num_slots, w_fp32, eps, stream)
 
 
+@functools.lru_cache(maxsize=None)  # a constant of the head dim
 def s2attn_cache_attn_workspace_bytes(D) -> int:
     return load().s2attn_cache_attn_workspace_bytes(D)
 

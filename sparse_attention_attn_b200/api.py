@@ -638,12 +638,11 @@ def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, n
 def _need_cache(k_cache, v_cache, Hkv, D, dev):
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [num_blocks, block_size, Hkv, D] tensor")
-    nb, bs = k_cache.shape[:2]
-    if Hkv is None:
-        Hkv = k_cache.shape[2]
-    _need("k_cache", k_cache, (nb, bs, Hkv, D), device=dev)
-    _need("v_cache", v_cache, (nb, bs, Hkv, D), device=dev)
-    return nb, bs, Hkv
+    nb, bs, heads, _ = k_cache.shape
+    shape = (nb, bs, heads if Hkv is None else Hkv, D)
+    _need("k_cache", k_cache, shape, torch.bfloat16, dev)
+    _need("v_cache", v_cache, shape, torch.bfloat16, dev)
+    return nb, bs, heads
 
 
 def cache_append(q, k, v, table, positions, slots, k_cache, v_cache, w_q=None, w_k=None, eps: float = 1e-6,

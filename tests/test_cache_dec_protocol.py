@@ -1,0 +1,173 @@
+"""A model of the few-row cache attention kernel's synchronisation
+(csrc/s2_cache_dec.cu), run on the CPU: the TMA producer with its two-slot ring of
+segment descriptions and query rows and its ring of K/V stages, the four consumer
+warps, their join through the last stage's memory (two halving steps between named
+barriers) and the copies in flight, interleaved at random with the kernel's
+arrival counts and phases.  It checks that every program finishes, that no parity
+wait is ahead of or overrun by its barrier, that every warp reads the stage and
+the segment it means, that the join's buffers are not written while a warp still
+reads the stage or the step before, and that no stage is refilled in use.  A
+segment is its number of stages; 0: nothing visible."""
+import random
+
+import pytest
+
+from tests.test_cache_attn_protocol import Bar
+
+WARPS = 4
+
+
+def run(segs, seed, NS=3, release_early=False):
+    rnd = random.Random(seed)
+    bars = {("sync", 0): Bar(WARPS)}
+    for s in range(NS):
+        bars[("full", s)], bars[("empty", s)] = Bar(1), Bar(WARPS)
+    for s in range(2):
+        bars[("qfull", s)], bars[("qempty", s)] = Bar(1), Bar(WARPS)
+    err, tma = [], []
+    ring, users = [None] * NS, [0] * NS       # stage contents, warps that still need them
+    slot, susers = [None, None], [0, 0]       # segment slots
+    using = {}                                # what a warp reads of the stage its segment ends in
+    sums = {}                                 # what the join's buffers of a stage hold
+
+    def producer():
+        L = qu = 0
+        for k, n in enumerate([*segs, -1]):
+            qs = qu & 1
+            if qu > 1:
+                yield ("wait", ("qempty", qs), (qu >> 1) - 1)
+            if susers[qs]:
+                err.append("segment slot overwritten")
+            slot[qs], susers[qs] = ("in flight" if n > 0 else k), WARPS
+
+            def land(qs=qs, k=k):
+                slot[qs] = k
+                bars[("qfull", qs)].arrive()
+            tma.append(land) if n > 0 else land()
+            yield ("pause",)
+            qu += 1
+            for i in range(max(n, 0)):
+                s, r = L % NS, L // NS
+                if r > 0:
+                    yield ("wait", ("empty", s), r - 1)
+                if users[s]:
+                    err.append(f"stage {s} refilled while {users[s]} warps need it")
+                ring[s], users[s] = "in flight", WARPS
+
+                def land(s=s, tile=(k, i)):
+                    ring[s] = tile
+                    bars[("full", s)].arrive()
+                tma.append(land)
+                L += 1
+
+    def consumer(w):
+        L = nsync = 0
+        for qu, n in enumerate([*segs, -1]):
+            qs = qu & 1
+            yield ("wait", ("qfull", qs), qu >> 1)
+            if slot[qs] != qu:
+                err.append(f"warp {w} reads segment {slot[qs]} for {qu}")
+            if n < 0:
+                return
+            susers[qs] -= 1
+            yield ("arrive", ("qempty", qs))
+            reading = None
+            for i in range(n):
+                s = L % NS
+                yield ("wait", ("full", s), L // NS)
+                if ring[s] != (qu, i):
+                    err.append(f"warp {w} reads {ring[s]} for {(qu, i)}")
+                L += 1
+                if i + 1 < n:
+                    users[s] -= 1
+                    yield ("arrive", ("empty", s))
+                    continue
+                reading = s
+                using[w] = (s, "stage")
+                if release_early:
+                    yield ("arrive", ("empty", s))
+                yield ("pause",)
+            if reading is None:
+                continue
+            s = reading
+            for half in (2, 1):
+                using.pop(w)             # done with the stage, or with the step before
+                yield ("arrive", ("sync", 0))
+                yield ("wait", ("sync", 0), nsync)
+                nsync += 1
+                using[w] = (s, None)
+                if half <= w < 2 * half:
+                    if any(u in ((s, "stage"), (s, w - half)) for u in using.values()):
+                        err.append(f"join of segment {qu} writes over {using}")
+                    sums[s, w - half] = (qu, w, half)
+                yield ("arrive", ("sync", 0))
+                yield ("wait", ("sync", 0), nsync)
+                nsync += 1
+                if w < half:
+                    using[w] = (s, w)
+                    if sums.get((s, w)) != (qu, w + half, half) or ring[s] != (qu, n - 1):
+                        err.append(f"warp {w} joins {sums.get((s, w))} in {ring[s]}")
+                    yield ("pause",)
+            using.pop(w)
+            users[s] -= 1
+            if not release_early:
+                yield ("arrive", ("empty", s))
+
+    actors = {"producer": producer(), **{f"warp {w}": consumer(w) for w in range(WARPS)}}
+    pending, finished = {n: None for n in actors}, set()
+    while not err:
+        runnable = [n for n in actors if n not in finished and
+                    (pending[n] is None or bars[pending[n][1]].done >= pending[n][2] + 1)]
+        choices = runnable + (["tma"] if tma else [])
+        if not choices:
+            if len(finished) == len(actors):
+                return []
+            return ["deadlock: " + ", ".join(f"{n} waits {pending[n]}" for n in actors if n not in finished)]
+        c = rnd.choice(choices)
+        if c == "tma":
+            tma.pop(rnd.randrange(len(tma)))()
+            continue
+        while True:
+            try:
+                op = next(actors[c])
+            except StopIteration:
+                finished.add(c)
+                pending[c] = None
+                break
+            if op[0] == "pause":
+                pending[c] = None
+                break
+            if op[0] == "arrive":
+                bars[op[1]].arrive()
+                pending[c] = None
+                break
+            done = bars[op[1]].done
+            if op[1][0] != "sync":  # a named barrier blocks until its own phase: no parity to mistake
+                if done < op[2]:
+                    return [f"{c}: parity wait ahead on {op[1]} (waits phase {op[2]}, {done} complete)"]
+                if done >= op[2] + 2:
+                    return [f"{c}: phase overrun on {op[1]}"]
+            if done >= op[2] + 1:
+                continue
+            pending[c] = op
+            break
+    return err[:3]
+
+
+def sequences():
+    out = [[n] for n in range(8)] + [[1] * 7, [2, 1] * 4, [0, 3, 0, 0, 1], [5, 0, 4]]
+    rnd = random.Random(11)
+    return out + [[rnd.choice([0, 1, 1, 2, 3, 6, 9]) for _ in range(rnd.randint(2, 8))] for _ in range(60)]
+
+
+@pytest.mark.parametrize("NS", [3, 6])
+def test_few_row_protocol_runs_clean(NS):
+    for segs in sequences():
+        for seed in range(8):
+            problems = run(segs, seed, NS)
+            assert not problems, (problems, segs, seed)
+
+
+def test_model_finds_a_stage_released_before_the_join():
+    """Releasing the last stage before the join that uses its memory: the check is not vacuous."""
+    assert any(run([4, 5, 3], seed, release_early=True) for seed in range(40))
