@@ -101,6 +101,8 @@ __device__ __forceinline__ bool locate(const CacheAttnArgs& a, int tokens, int m
   run.u0 = run.per * blockIdx.x;
   run.u1 = min(run.u0 + run.per, total);
   if (run.u0 >= run.u1) return false;
+  if (tid == 0) found[0] = a.R, found[1] = 0;
+  __syncthreads();
   long long before = 0;
   for (int base = 0; base < a.R; base += THREADS) {
     if (a.R > THREADS) {  // one chunk: its scan is still there
@@ -121,13 +123,22 @@ __device__ __forceinline__ bool locate(const CacheAttnArgs& a, int tokens, int m
   return true;
 }
 
+// The next segment of the run; false at its end.  Called by a whole warp with the
+// same arguments: its lanes look for the next request with new tokens together.
 template <int KEYS>
 __device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, int tokens, Run& w, Seg& s) {
-  while (w.u0 < w.u1) {
+  while (w.u0 < w.u1 && w.ri < a.R) {  // (the second holds unless lengths change under the kernel)
     const Req r = request<KEYS>(a, w.ri, tokens);
     if (w.u0 >= w.rbase + r.units) {
       w.rbase += r.units;
-      ++w.ri;
+      for (++w.ri; w.ri < a.R; w.ri += 32) {
+        const int i = w.ri + (threadIdx.x & 31);
+        const unsigned busy = __ballot_sync(0xffffffffu, i < a.R && request<KEYS>(a, i, tokens).units > 0);
+        if (busy != 0) {
+          w.ri += __ffs(busy) - 1;
+          break;
+        }
+      }
       continue;
     }
     const long long in = w.u0 - w.rbase, item = in / r.kt;  // item = kvh * ni + item of the kv head

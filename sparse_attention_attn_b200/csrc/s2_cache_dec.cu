@@ -72,9 +72,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// Barrier of the consumer warps alone.
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
-
 // Address of 16-byte chunk c of row r in slabs of `slab` bytes written by TMA
 // with the 128-byte swizzle (slabs 1024-byte aligned).
 __device__ __forceinline__ uint32_t swz(uint32_t base, int slab, int r, int c) {
@@ -90,7 +87,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_qfull[2], bar_qempty[2];
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_qfull[2], bar_qempty[2], bar_join;
   __shared__ uint32_t abort_flag;
   __shared__ long long sums[kDecThreads / 32], found[2];
   __shared__ Seg segs[2];
@@ -111,6 +108,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       mbar_init(smem_u32(&bar_qfull[s]), 1);
       mbar_init(smem_u32(&bar_qempty[s]), kWarps);
     }
+    mbar_init(smem_u32(&bar_join), kWarps);
     fence_barrier_init();
   }
   __syncthreads();
@@ -174,7 +172,14 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   } else {
     // ------------------------------------------------------------ consumers
     const float sl2 = a.scale_log2;
-    int L = 0;
+    int L = 0, nj = 0;
+    // the four warps meet (a bounded wait, where a named barrier would block for
+    // good once a warp has given up)
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_join));
+      return warp_wait(smem_u32(&bar_join), nj++ & 1, wc, 144);
+    };
     for (int qu = 0;; ++qu) {
       const int qs = qu & 1;
       if (!warp_wait(smem_u32(&bar_qfull[qs]), (qu >> 1) & 1, wc, 142)) break;
@@ -190,14 +195,6 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar_qempty[qs]));
       const int rows = sg.ntok * a.rep;
-      int last_key[2];  // chains: the last key of the lane's two rows
-      unsigned long long see[2] = {0, 0};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = (lane >> 2) + 8 * h, j = row < rows ? sg.tok + row / a.rep : sg.tok;
-        last_key[h] = min(sg.ctx + j, sg.keys - 1);
-        if (a.mask != nullptr) see[h] = visible_drafts(a, sg, sg.row0 + j);
-      }
       float o[D / 8][4];
 #pragma unroll
       for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
@@ -221,13 +218,20 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           }
           if (key0 + 16 > sg.ctx) {  // some key of the warp is a draft or behind the last
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int h = 0; h < 2; ++h) {
+              // what the lane's row sees: up to its last key (chains), or the draft bits
+              const int row = (lane >> 2) + 8 * h, j = sg.tok + (row < rows ? row / a.rep : 0);
+              const int last_key = min(sg.ctx + j, sg.keys - 1);
+              const unsigned long long see = a.mask != nullptr ? visible_drafts(a, sg, sg.row0 + j) : 0ull;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = key0 + n * 8 + (lane & 3) * 2 + (e & 1), h = e >> 1, d = key - sg.ctx;
-                const bool vis = a.mask == nullptr ? key <= last_key[h] : d < 0 || (d < 64 && (see[h] >> (d & 63) & 1));
-                if (!vis) sc[n][e] = neg_inf();
-              }
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int key = key0 + n * 8 + (lane & 3) * 2 + e, d = key - sg.ctx;
+                  const bool vis = a.mask == nullptr ? key <= last_key : d < 0 || (d < 64 && (see >> (d & 63) & 1));
+                  if (!vis) sc[n][2 * h + e] = neg_inf();
+                }
+            }
           }
           uint32_t pf[4];
           float alpha[2];
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         float* jm = jo + 2 * kRows * C::JROW;                       // [2][row] maxima, then sums
 #pragma unroll
         for (int half = 2; half > 0; half >>= 1) {
-          consumer_sync();  // the stage (or the buffers of the step before) have been read
+          if (!(ok = meet())) break;  // the stage (or the buffers of the step before) have been read
           if (warp >= half && warp < 2 * half) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               }
             }
           }
-          consumer_sync();
+          if (!(ok = meet())) break;
           if (warp < half) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -363,6 +367,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
             }
           }
         }
+        if (!ok) break;
         fence_proxy_async_smem();  // these accesses before the TMA that refills the stage
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));

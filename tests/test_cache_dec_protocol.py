@@ -1,8 +1,8 @@
 """A model of the few-row cache attention kernel's synchronisation
 (csrc/s2_cache_dec.cu), run on the CPU: the TMA producer with its two-slot ring of
 segment descriptions and query rows and its ring of K/V stages, the four consumer
-warps, their join through the last stage's memory (two halving steps between named
-barriers) and the copies in flight, interleaved at random with the kernel's
+warps, their join through the last stage's memory (two halving steps between
+meetings of the warps) and the copies in flight, interleaved at random with the kernel's
 arrival counts and phases.  It checks that every program finishes, that no parity
 wait is ahead of or overrun by its barrier, that every warp reads the stage and
 the segment it means, that the join's buffers are not written while a warp still
@@ -142,11 +142,10 @@ def run(segs, seed, NS=3, release_early=False):
                 pending[c] = None
                 break
             done = bars[op[1]].done
-            if op[1][0] != "sync":  # a named barrier blocks until its own phase: no parity to mistake
-                if done < op[2]:
-                    return [f"{c}: parity wait ahead on {op[1]} (waits phase {op[2]}, {done} complete)"]
-                if done >= op[2] + 2:
-                    return [f"{c}: phase overrun on {op[1]}"]
+            if done < op[2]:
+                return [f"{c}: parity wait ahead on {op[1]} (waits phase {op[2]}, {done} complete)"]
+            if done >= op[2] + 2:
+                return [f"{c}: phase overrun on {op[1]}"]
             if done >= op[2] + 1:
                 continue
             pending[c] = op

@@ -177,7 +177,7 @@ def _tree_masks(lens, seed, drop=0.0):
 LENS = {
     "one": [(0, 1)], "first-key": [(1, 1)], "tile-edges": [(63, 1), (64, 1), (65, 1), (127, 1), (128, 1), (15, 1), (16, 1)],
     "long": [(5000, 1)], "ragged": [(17, 3), (700, 1), (0, 5), (333, 2), (1, 1), (64, 64)], "gaps": [(10, 0), (30, 2), (0, 0), (5, 4), (9, 0)],
-    "chunk": [(100, 200), (0, 130)], "many": [(3 * i % 97, i % 3) for i in range(300)], "drafts": [(900, 61), (127, 64), (3, 7)],
+    "chunk": [(100, 200), (0, 130)], "many": [(3 * i % 97, i % 3) for i in range(300)], "sparse": [(40 + i, int(i % 71 == 5)) for i in range(500)], "drafts": [(900, 61), (127, 64), (3, 7)],
 }
 
 
