@@ -12,11 +12,40 @@ attention.  Training uses the shifted groups, inference the dense path.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib
+
+
+class _Binding:
+    """The calls of _s2torch.so (csrc/s2_torch.cpp: the usual case of the smallest
+    calls in one step, None for any other), bound at the first use to the library
+    the ctypes binding loaded; where it is not built or does not load, functions
+    that leave every call to the Python path."""
+
+    _NAMES = ("qknorm_fwd", "qknorm_bwd", "cache_append", "cache_plan", "cache_attention")
+
+    def __getattr__(self, name):
+        if name not in self._NAMES:
+            raise AttributeError(name)
+        lib = _lib.load()
+        try:
+            from . import _s2torch
+            _s2torch.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                            ("s2attn_qknorm_rope_fwd", "s2attn_qknorm_rope_bwd",
+                             "s2attn_qknorm_rope_bwd_workspace_bytes", "s2attn_cache_append", "s2attn_cache_plan",
+                             "s2attn_cache_attn", "s2attn_cache_attn_workspace_bytes")))
+            calls = {n: getattr(_s2torch, n) for n in self._NAMES}
+        except ImportError:
+            calls = {n: lambda *args: None for n in self._NAMES}
+        self.__dict__.update(calls)
+        return calls[name]
+
+
+_fast = _Binding()
 
 
 def _stream(device=None) -> int:
@@ -499,6 +528,10 @@ def qknorm_rope_forward(q, k, w_q, w_k, table, eps: float = 1e-6, q_out=None, k_
     w_k ([D], fp32 or bf16), and the rotation by the table, in one pass.
     q [B, N, H, D], k [B, N, Hkv, D] bf16; any N.  Returns (q_out, k_out), which
     s2attn_forward takes; q_out may be q and k_out may be k (in place)."""
+    if q_out is None and k_out is None:
+        r = _fast.qknorm_fwd(q, k, w_q, w_k, table, eps)
+        if r is not None:
+            return r
     B, N, H, Hkv, D = _dims(q, k)
     _need("q", q, (B, N, H, D))
     dev = q.device
@@ -517,6 +550,10 @@ def qknorm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, table, eps: float = 1e-
     """Backward of qknorm_rope_forward from its inputs and the gradients of its
     outputs.  Returns (dq, dk, dw_q, dw_k); the weight gradients have the
     weights' type.  dq may be dq_out and dk may be dk_out (in place)."""
+    if dq is None and dk is None and dw_q is None and dw_k is None and workspace is None:
+        r = _fast.qknorm_bwd(q, k, w_q, w_k, dq_out, dk_out, table, eps)
+        if r is not None:
+            return r
     B, N, H, Hkv, D = _dims(q, k)
     _need("q", q, (B, N, H, D))
     dev = q.device
@@ -608,6 +645,9 @@ def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, n
     int32 [num_tokens]: the new tokens of each request are a tree of drafts,
     parents[t] the index in the request of the draft before it, -1 for the
     context.  Returns a CachePlan."""
+    r = _fast.cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size, num_tokens, parents)
+    if r is not None:
+        return CachePlan(*r)
     if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
         raise ValueError("ctx_lens must be an int32 tensor [R]")
     R, T = ctx_lens.shape[0], int(num_tokens)
@@ -654,6 +694,9 @@ def cache_append(q, k, v, table, positions, slots, k_cache, v_cache, w_q=None, w
     Hkv, D] bf16) at slots (int32 [T]).  Tokens with a negative slot are
     padding: nothing is written for them.  No two tokens may share a slot.
     Returns q_out (may be q)."""
+    r = _fast.cache_append(q, k, v, table, positions, slots, k_cache, v_cache, w_q, w_k, eps, q_out)
+    if r is not None:
+        return r
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, H, D] and k [T, Hkv, D]")
     T, H, D = q.shape
@@ -690,6 +733,10 @@ def cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mas
     new ones, those its mask (int64 [T], bit j = new token j) names -- without
     mask those up to its own.  Returns (o [T, H, D] bf16, lse [H, T] fp32); rows
     that see no key get 0 and -inf, rows of no request are left as they are."""
+    if out is None and lse is None and workspace is None:
+        r = _fast.cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mask)
+        if r is not None:
+            return r
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [T, H, D] tensor")
     T, H, D = q.shape

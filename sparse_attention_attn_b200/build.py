@@ -7,14 +7,20 @@
 The library is plain CUDA C++ compiled by nvcc; it links only the CUDA runtime
 (statically) and resolves cuTensorMapEncodeTiled through the runtime's driver
 entry-point query, so it needs no libcuda at link time.
+
+Beside it, _s2torch.so: a small CPython extension (g++, torch's headers) that
+shortens the Python side of the smallest calls.  Where it cannot be built the
+package works without it.
 """
 from __future__ import annotations
 
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +28,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libs2attn.so")
 LIB_DEBUG = os.path.join(PKG, "libs2attn_debug.so")
+BINDING = os.path.join(PKG, "_s2torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "s2_torch.cpp")
 
 SOURCES = ["s2attn.cu", "s2_fwd.cu", "s2_fwd64.cu", "s2_bwd.cu", "s2_bwd_fused.cu", "s2_rope.cu", "s2_segment.cu", "s2_nf4.cu", "s2_bwd_ds.cu", "s2_bwd_kv128.cu",
            "s2_qknorm.cu", "s2_cache.cu", "s2_cache_dec.cu", "s2_cache_tc.cu"]
@@ -52,7 +60,13 @@ def source_hash(debug: bool = False) -> str:
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile libs2attn.so (or, with debug, libs2attn_debug.so: the same
     sources with the kernels' index checks compiled in) unless an up-to-date
-    build exists.  Returns its path.  The sources compile in parallel."""
+    build exists, and with it _s2torch.so.  Returns its path.  The sources
+    compile in parallel."""
+    if not debug:
+        try:
+            build_binding(force)
+        except (OSError, subprocess.CalledProcessError) as e:
+            print(f"warning: _s2torch.so was not built ({e}); the Python path serves alone", file=sys.stderr)
     lib = LIB_DEBUG if debug else LIB
     stamp = lib + ".srchash"
     digest = source_hash(debug)
@@ -84,6 +98,40 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     with open(stamp, "w") as fh:
         fh.write(digest)
     return lib
+
+
+def build_binding(force: bool = False):
+    """Compile _s2torch.so unless an up-to-date build exists.  Returns its
+    path, or None where a compiler or headers are missing (torch is located, not
+    imported)."""
+    spec = importlib.util.find_spec("torch")
+    gxx, python_h = shutil.which("g++"), sysconfig.get_paths()["include"]
+    cuda_h = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
+    if spec is None or spec.origin is None or gxx is None:
+        return None
+    torch_dir = os.path.dirname(spec.origin)
+    torch_h, version = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "version.py")
+    if not all(map(os.path.exists, (os.path.join(python_h, "Python.h"), os.path.join(torch_h, "ATen", "ATen.h"), version,
+                                    os.path.join(cuda_h, "cuda_runtime.h")))):
+        return None
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I" + INCLUDE, "-I" + python_h,
+           "-I" + torch_h, "-I" + os.path.join(torch_h, "torch", "csrc", "api", "include"), "-I" + cuda_h, BINDING_SOURCE,
+           "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    h = hashlib.sha256(" ".join(cmd).encode() + sys.version.encode())
+    for f in (BINDING_SOURCE, os.path.join(INCLUDE, "s2attn.h"), version):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    stamp = BINDING + ".srchash"
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp):
+        with open(stamp) as fh:
+            if fh.read().strip() == h.hexdigest():
+                return BINDING
+    tmp = BINDING + ".tmp"
+    subprocess.run(cmd + ["-o", tmp], check=True)
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as fh:
+        fh.write(h.hexdigest())
+    return BINDING
 
 
 if __name__ == "__main__":
