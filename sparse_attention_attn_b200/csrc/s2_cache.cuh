@@ -288,11 +288,6 @@ struct Part {
   }
 };
 
-// Lets the dependent launch begin (its blocks wait for this grid's end where
-// they need its results), and that wait.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The join work of CTA blockIdx.x: an item that begins in it and runs on.
 __device__ __forceinline__ int4 join_work(const Seg& s) {
   return make_int4(s.row0 + s.tok, s.ntok, s.kvh, s.last_cta);
@@ -411,17 +406,9 @@ __global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a) {
 // The join as a dependent launch of the attention kernel before it in the stream.
 template <int ROWS, int TILE, int D, int WPR, int RPW>
 cudaError_t launch_join(const CacheAttnArgs& a, int grid, cudaStream_t stream) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, ROWS * WPR / (8 * RPW));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   prof_before(stream, kKernelCacheMerge);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<ROWS, TILE, D, WPR, RPW>, a);
+  const cudaError_t e =
+      launch_dependent(s2_cache_join_kernel<ROWS, TILE, D, WPR, RPW>, dim3(grid, ROWS * WPR / (8 * RPW)), 256, stream, a);
   prof_after(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

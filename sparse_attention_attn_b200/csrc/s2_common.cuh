@@ -455,7 +455,8 @@ struct QkNormArgs {
   __nv_bfloat16 *yq, *yk;          // forward: rotated q, k; backward: gradients of q, k
   const void *wq, *wk;             // norm weights [D]
   const float2* table;             // (cos, sin) [N][D/2]
-  float* partial;                  // backward: [blocks][2][D] partial weight gradients
+  float* partial;                  // backward: [blocks][D] partial weight gradients
+  int blocks_q, blocks;            // backward: blocks that take query rows, and all
   void *dwq, *dwk;                 // backward: weight gradients [D]
   int tokens, N, H, Hkv;           // tokens = B N
   float eps;
@@ -537,5 +538,21 @@ enum KernelId : int {
 };
 void prof_before(cudaStream_t stream, int kernel_id);
 void prof_after(cudaStream_t stream);
+
+// Launches a kernel that waits (griddepcontrol.wait) for the one before it in
+// the stream, so that its launch overlaps that one's end.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 }  // namespace s2

@@ -189,100 +189,105 @@ __global__ void __launch_bounds__(256) s2_qknorm_fwd_kernel(QkNormArgs a) {
   }
 }
 
-// Backward.  The same units, the query rows and then the key rows, HG heads at
-// a time; a thread keeps the sums of du r x of its 16 columns in registers,
-// and the block leaves one partial row per weight in the workspace.
+// Backward.  The same units; the first blocks take the query rows and the others
+// the key rows, HG heads of a token at a time.  A thread keeps the sums of du r x
+// of its 16 columns in registers, and the block leaves a partial row in the
+// workspace.  Two blocks an SM (128 registers a thread) with two heads a thread
+// keep 64 KB of loads in flight there; at 32768 tokens x 72 heads of 128: 297-308
+// us of 280 at the measured copy bandwidth.  Measured on the way: 409 us with one
+// block an SM, 342 with four heads a thread, 580 with one head and three blocks
+// (spills), 382 with chunks bulk-copied through a shared-memory ring, whose extra
+// instructions cost more than the loads in flight gave.
 template <int D, typename W, int HG>
 __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
   constexpr int CH = D / 16;
   __shared__ float red[8][D];
+  launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = lane % CH;
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int heads = which ? a.Hkv : a.H;
-    const __nv_bfloat16* x = which ? a.k : a.q;
-    const __nv_bfloat16* dy = which ? a.gk : a.gq;
-    __nv_bfloat16* dx = which ? a.yk : a.yq;
-    const W* w = static_cast<const W*>(which ? a.wk : a.wq);
-    const Oct w1 = load_oct(w, ch * 8), w2 = load_oct(w, ch * 8 + D / 2);
-    Oct acc1 = {{0ull, 0ull, 0ull, 0ull}}, acc2 = acc1;
-    const int G = (heads + HG - 1) / HG;
-    const long long n = static_cast<long long>(a.tokens) * G * CH;
-    for (long long e0 = blockIdx.x * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += gridDim.x * 256LL) {
-      const long long e = e0 + lane;
-      const bool live = e < n;
-      const uint32_t unit = live ? static_cast<uint32_t>(e / CH) : 0u;
-      const int tok = unit / G, h0 = (unit - tok * G) * HG;
-      const size_t off = (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
-      uint4 u1[HG], u2[HG], d1[HG], d2[HG];
+  const bool which = static_cast<int>(blockIdx.x) >= a.blocks_q;  // key rows
+  const int block = which ? blockIdx.x - a.blocks_q : blockIdx.x, grid = which ? a.blocks - a.blocks_q : a.blocks_q;
+  const int heads = which ? a.Hkv : a.H;
+  const __nv_bfloat16* x = which ? a.k : a.q;
+  const __nv_bfloat16* dy = which ? a.gk : a.gq;
+  __nv_bfloat16* dx = which ? a.yk : a.yq;
+  const W* w = static_cast<const W*>(which ? a.wk : a.wq);
+  const Oct w1 = load_oct(w, ch * 8), w2 = load_oct(w, ch * 8 + D / 2);
+  Oct acc1 = {{0ull, 0ull, 0ull, 0ull}}, acc2 = acc1;
+  const int G = (heads + HG - 1) / HG;
+  const long long n = static_cast<long long>(a.tokens) * G * CH;
+  for (long long e0 = block * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += grid * 256LL) {
+    const long long e = e0 + lane;
+    const bool live = e < n;
+    const uint32_t unit = live ? static_cast<uint32_t>(e / CH) : 0u;
+    const int tok = unit / G, h0 = (unit - tok * G) * HG;
+    const size_t off = (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
+    uint4 u1[HG], u2[HG], d1[HG], d2[HG];
 #pragma unroll
-      for (int k = 0; k < HG; ++k) {
-        u1[k] = u2[k] = d1[k] = d2[k] = make_uint4(0, 0, 0, 0);
-        if (live && h0 + k < heads) {
-          u1[k] = *reinterpret_cast<const uint4*>(x + off + k * D);
-          u2[k] = *reinterpret_cast<const uint4*>(x + off + k * D + D / 2);
-          d1[k] = *reinterpret_cast<const uint4*>(dy + off + k * D);
-          d2[k] = *reinterpret_cast<const uint4*>(dy + off + k * D + D / 2);
-        }
-      }
-      Oct c, s, ns;
-      load_turn_oct(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s, ns);
-#pragma unroll
-      for (int k = 0; k < HG; ++k) {
-        const Oct x1 = unpack_oct(u1[k]), x2 = unpack_oct(u2[k]);
-        Oct g1 = unpack_oct(d1[k]), g2 = unpack_oct(d2[k]);
-        const float r = row_rms<D>(x1, x2, a.eps);
-        const uint64_t r2 = f2_pack(r, r);
-        uint64_t sa = 0ull, sb = 0ull;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // du, then dw += du r x, g = du w, sum of g x
-          const uint64_t du1 = f2_fma(g2.v[j], s.v[j], f2_mul(g1.v[j], c.v[j]));
-          const uint64_t du2 = f2_fma(g1.v[j], ns.v[j], f2_mul(g2.v[j], c.v[j]));
-          acc1.v[j] = f2_fma(du1, f2_mul(r2, x1.v[j]), acc1.v[j]);
-          acc2.v[j] = f2_fma(du2, f2_mul(r2, x2.v[j]), acc2.v[j]);
-          g1.v[j] = f2_mul(du1, w1.v[j]);
-          g2.v[j] = f2_mul(du2, w2.v[j]);
-          sa = f2_fma(g1.v[j], x1.v[j], sa);
-          sb = f2_fma(g2.v[j], x2.v[j], sb);
-        }
-        const float nm = row_sum<CH>(f2_sum(f2_add(sa, sb))) * (-1.f / D) * r * r * r;
-        const uint64_t nm2 = f2_pack(nm, nm);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // dx = r g - r^3 mean(g x) x
-          g1.v[j] = f2_fma(x1.v[j], nm2, f2_mul(r2, g1.v[j]));
-          g2.v[j] = f2_fma(x2.v[j], nm2, f2_mul(r2, g2.v[j]));
-        }
-        if (live && h0 + k < heads) {
-          *reinterpret_cast<uint4*>(dx + off + k * D) = pack8(g1);
-          *reinterpret_cast<uint4*>(dx + off + k * D + D / 2) = pack8(g2);
-        }
+    for (int k = 0; k < HG; ++k) {
+      u1[k] = u2[k] = d1[k] = d2[k] = make_uint4(0, 0, 0, 0);
+      if (live && h0 + k < heads) {
+        u1[k] = *reinterpret_cast<const uint4*>(x + off + k * D);
+        u2[k] = *reinterpret_cast<const uint4*>(x + off + k * D + D / 2);
+        d1[k] = *reinterpret_cast<const uint4*>(dy + off + k * D);
+        d2[k] = *reinterpret_cast<const uint4*>(dy + off + k * D + D / 2);
       }
     }
+    Oct c, s, ns;
+    load_turn_oct(a.table, static_cast<size_t>(tok % a.N) * (D / 2) + ch * 8, c, s, ns);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // lanes of equal chunk, then the block's warps
+    for (int k = 0; k < HG; ++k) {
+      const Oct x1 = unpack_oct(u1[k]), x2 = unpack_oct(u2[k]);
+      Oct g1 = unpack_oct(d1[k]), g2 = unpack_oct(d2[k]);
+      const float r = row_rms<D>(x1, x2, a.eps);
+      const uint64_t r2 = f2_pack(r, r);
+      uint64_t sa = 0ull, sb = 0ull;
 #pragma unroll
-      for (int m = CH; m < 32; m <<= 1) {
-        acc1.v[j] = f2_add(acc1.v[j], __shfl_xor_sync(0xffffffffu, acc1.v[j], m));
-        acc2.v[j] = f2_add(acc2.v[j], __shfl_xor_sync(0xffffffffu, acc2.v[j], m));
+      for (int j = 0; j < 4; ++j) {  // du, then dw += du r x, g = du w, sum of g x
+        const uint64_t du1 = f2_fma(g2.v[j], s.v[j], f2_mul(g1.v[j], c.v[j]));
+        const uint64_t du2 = f2_fma(g1.v[j], ns.v[j], f2_mul(g2.v[j], c.v[j]));
+        acc1.v[j] = f2_fma(du1, f2_mul(r2, x1.v[j]), acc1.v[j]);
+        acc2.v[j] = f2_fma(du2, f2_mul(r2, x2.v[j]), acc2.v[j]);
+        g1.v[j] = f2_mul(du1, w1.v[j]);
+        g2.v[j] = f2_mul(du2, w2.v[j]);
+        sa = f2_fma(g1.v[j], x1.v[j], sa);
+        sb = f2_fma(g2.v[j], x2.v[j], sb);
+      }
+      const float nm = row_sum<CH>(f2_sum(f2_add(sa, sb))) * (-1.f / D) * r * r;
+      const uint64_t nm2 = f2_pack(nm, nm);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // dx = r (g - r^2 mean(g x) x)
+        g1.v[j] = f2_mul(r2, f2_fma(x1.v[j], nm2, g1.v[j]));
+        g2.v[j] = f2_mul(r2, f2_fma(x2.v[j], nm2, g2.v[j]));
+      }
+      if (live && h0 + k < heads) {
+        *reinterpret_cast<uint4*>(dx + off + k * D) = pack8(g1);
+        *reinterpret_cast<uint4*>(dx + off + k * D + D / 2) = pack8(g2);
       }
     }
-    __syncthreads();  // red[] of the query pass has been read
-    if (lane < CH) {
+  }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        red[warp][ch * 8 + 2 * j] = f2_lo(acc1.v[j]);
-        red[warp][ch * 8 + 2 * j + 1] = f2_hi(acc1.v[j]);
-        red[warp][ch * 8 + D / 2 + 2 * j] = f2_lo(acc2.v[j]);
-        red[warp][ch * 8 + D / 2 + 2 * j + 1] = f2_hi(acc2.v[j]);
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float t = 0.f;
+  for (int j = 0; j < 4; ++j) {  // lanes of equal chunk, then the block's warps
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
-      a.partial[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + threadIdx.x] = t;
+    for (int m = CH; m < 32; m <<= 1) {
+      acc1.v[j] = f2_add(acc1.v[j], __shfl_xor_sync(0xffffffffu, acc1.v[j], m));
+      acc2.v[j] = f2_add(acc2.v[j], __shfl_xor_sync(0xffffffffu, acc2.v[j], m));
     }
+  }
+  if (lane < CH) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      red[warp][ch * 8 + 2 * j] = f2_lo(acc1.v[j]);
+      red[warp][ch * 8 + 2 * j + 1] = f2_hi(acc1.v[j]);
+      red[warp][ch * 8 + D / 2 + 2 * j] = f2_lo(acc2.v[j]);
+      red[warp][ch * 8 + D / 2 + 2 * j + 1] = f2_hi(acc2.v[j]);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
+    a.partial[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = t;
   }
 }
 
@@ -292,19 +297,22 @@ __device__ __forceinline__ void store_w(float* p, int i, double v) { p[i] = stat
 __device__ __forceinline__ void store_w(__nv_bfloat16* p, int i, double v) { p[i] = __double2bfloat16(v); }
 
 template <int D, typename W>
-__global__ void __launch_bounds__(1024) s2_qknorm_dw_kernel(QkNormArgs a, int blocks) {
+__global__ void __launch_bounds__(1024) s2_qknorm_dw_kernel(QkNormArgs a) {
   __shared__ double red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;  // column of [2][D]
+  const bool which = blockIdx.x >= D / 32;
+  const int col = blockIdx.x % (D / 32) * 32 + lane;
+  wait_for_primary();
   double t = 0.0;
-  for (int b = warp; b < blocks; b += 32) t += a.partial[static_cast<size_t>(b) * 2 * D + col];
+  for (int b = (which ? a.blocks_q : 0) + warp; b < (which ? a.blocks : a.blocks_q); b += 32)
+    t += a.partial[static_cast<size_t>(b) * D + col];
   red[warp][lane] = t;
   __syncthreads();
   if (warp == 0) {
     t = 0.0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) t += red[i][lane];
-    store_w(static_cast<W*>(col < D ? a.dwq : a.dwk), col % D, t);
+    store_w(static_cast<W*>(which ? a.dwk : a.dwq), col, t);
   }
 }
 
@@ -375,13 +383,32 @@ void fwd_launch(const QkNormArgs& a, int num_sms, cudaStream_t stream) {
 }
 
 template <int D, typename W>
-int bwd_launch(const QkNormArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t bwd_launch(QkNormArgs a, int num_sms, cudaStream_t stream) {
   constexpr int HG = 2;
-  const long long n = static_cast<long long>(a.tokens) * ((a.H + HG - 1) / HG) * (D / 16);
-  int blocks = blocks_for(n, num_sms, 4);
-  if (blocks > kQkNormMaxBlocks) blocks = kQkNormMaxBlocks;
-  s2_qknorm_bwd_kernel<D, W, HG><<<blocks, 256, 0, stream>>>(a);
-  return blocks;
+  // blocks in proportion to the rows of either kind, at most 4 an SM in all (two
+  // run at a time) and no more than the workspace holds
+  const long long nq = static_cast<long long>(a.tokens) * ((a.H + HG - 1) / HG) * (D / 16);
+  const long long nk = static_cast<long long>(a.tokens) * ((a.Hkv + HG - 1) / HG) * (D / 16);
+  const long long bq = (nq + 255) / 256, bk = (nk + 255) / 256;
+  const long long most = num_sms * 4 < kQkNormMaxBlocks ? num_sms * 4 : kQkNormMaxBlocks;
+  if (bq + bk <= most) {
+    a.blocks_q = static_cast<int>(bq);
+    a.blocks = static_cast<int>(bq + bk);
+  } else {
+    const double part = static_cast<double>(nq) / static_cast<double>(nq + nk);
+    const int share = static_cast<int>(part * static_cast<double>(most) + 0.5);
+    a.blocks = static_cast<int>(most);
+    a.blocks_q = share < 1 ? 1 : (share > a.blocks - 1 ? a.blocks - 1 : share);
+  }
+  prof_before(stream, kKernelQkNormBwd);
+  s2_qknorm_bwd_kernel<D, W, HG><<<a.blocks, 256, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  prof_after(stream);
+  if (e != cudaSuccess) return e;
+  prof_before(stream, kKernelQkNormDw);
+  e = launch_dependent(s2_qknorm_dw_kernel<D, W>, dim3(2 * D / 32), 1024, stream, a);
+  prof_after(stream);
+  return e;
 }
 
 template <int D, typename W>
@@ -409,30 +436,9 @@ cudaError_t launch_qknorm_fwd(const QkNormArgs& a, int D, int w_fp32, int num_sm
 }
 
 cudaError_t launch_qknorm_bwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream) {
-  prof_before(stream, kKernelQkNormBwd);
-  int blocks;
   if (D == 64)
-    blocks = w_fp32 ? bwd_launch<64, float>(a, num_sms, stream) : bwd_launch<64, __nv_bfloat16>(a, num_sms, stream);
-  else
-    blocks = w_fp32 ? bwd_launch<128, float>(a, num_sms, stream) : bwd_launch<128, __nv_bfloat16>(a, num_sms, stream);
-  cudaError_t e = cudaGetLastError();
-  prof_after(stream);
-  if (e != cudaSuccess) return e;
-  prof_before(stream, kKernelQkNormDw);
-  if (D == 64) {
-    if (w_fp32)
-      s2_qknorm_dw_kernel<64, float><<<4, 1024, 0, stream>>>(a, blocks);
-    else
-      s2_qknorm_dw_kernel<64, __nv_bfloat16><<<4, 1024, 0, stream>>>(a, blocks);
-  } else {
-    if (w_fp32)
-      s2_qknorm_dw_kernel<128, float><<<8, 1024, 0, stream>>>(a, blocks);
-    else
-      s2_qknorm_dw_kernel<128, __nv_bfloat16><<<8, 1024, 0, stream>>>(a, blocks);
-  }
-  e = cudaGetLastError();
-  prof_after(stream);
-  return e;
+    return w_fp32 ? bwd_launch<64, float>(a, num_sms, stream) : bwd_launch<64, __nv_bfloat16>(a, num_sms, stream);
+  return w_fp32 ? bwd_launch<128, float>(a, num_sms, stream) : bwd_launch<128, __nv_bfloat16>(a, num_sms, stream);
 }
 
 cudaError_t launch_cache_append(const CacheAppendArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream) {
