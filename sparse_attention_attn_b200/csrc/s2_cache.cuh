@@ -61,14 +61,22 @@ struct Seg {
 struct Run {
   long long u0, u1, rbase, per;  // units left; first unit of request ri; units of a run
   int ri;
+  Req r;                         // request ri (ri < R)
+};
+// What the CTA's threads share while they look for its first request.
+struct Found {
+  long long rbase;
+  int ri;
+  Req r;
 };
 
 // Finds the run of this CTA and the request it begins in; false if it has no
 // units.  All THREADS threads of the block call it; `sums` and `found` are
-// shared memory.
+// shared memory.  (The first request comes out of it as it was scanned: reading
+// it again would cost every CTA's first load another trip to L2.)
 template <int THREADS, int KEYS>
 __device__ __forceinline__ bool locate(const CacheAttnArgs& a, int tokens, int min_units, long long* sums,
-                                       long long* found, Run& run) {
+                                       Found* found, Run& run) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // exclusive prefix of v over the block, and the block's sum
   auto scan = [&](long long v, long long& all) {
@@ -91,9 +99,11 @@ __device__ __forceinline__ bool locate(const CacheAttnArgs& a, int tokens, int m
     return base + inc - v;
   };
   long long total = 0, mine = 0, at = 0;
+  Req r = {};
   for (int base = 0; base < a.R; base += THREADS) {
     long long all;
-    mine = base + tid < a.R ? request<KEYS>(a, base + tid, tokens).units : 0;
+    if (base + tid < a.R) r = request<KEYS>(a, base + tid, tokens);
+    mine = base + tid < a.R ? r.units : 0;
     at = total + scan(mine, all);
     total += all;
   }
@@ -101,25 +111,28 @@ __device__ __forceinline__ bool locate(const CacheAttnArgs& a, int tokens, int m
   run.u0 = run.per * blockIdx.x;
   run.u1 = min(run.u0 + run.per, total);
   if (run.u0 >= run.u1) return false;
-  if (tid == 0) found[0] = a.R, found[1] = 0;
+  if (tid == 0) found->ri = a.R;
   __syncthreads();
   long long before = 0;
   for (int base = 0; base < a.R; base += THREADS) {
     if (a.R > THREADS) {  // one chunk: its scan is still there
       long long all;
-      mine = base + tid < a.R ? request<KEYS>(a, base + tid, tokens).units : 0;
+      if (base + tid < a.R) r = request<KEYS>(a, base + tid, tokens);
+      mine = base + tid < a.R ? r.units : 0;
       at = before + scan(mine, all);
       before += all;
     }
     if (run.u0 >= at && run.u0 < at + mine) {
-      found[0] = base + tid;
-      found[1] = at;
+      found->ri = base + tid;
+      found->rbase = at;
+      found->r = r;
     }
     if (a.R > THREADS && run.u0 < before) break;  // uniform
   }
   __syncthreads();
-  run.ri = static_cast<int>(found[0]);
-  run.rbase = found[1];
+  run.ri = found->ri;
+  run.rbase = found->rbase;
+  run.r = found->r;
   return true;
 }
 
@@ -128,7 +141,7 @@ __device__ __forceinline__ bool locate(const CacheAttnArgs& a, int tokens, int m
 template <int KEYS>
 __device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, int tokens, Run& w, Seg& s) {
   while (w.u0 < w.u1 && w.ri < a.R) {  // (the second holds unless lengths change under the kernel)
-    const Req r = request<KEYS>(a, w.ri, tokens);
+    const Req& r = w.r;
     if (w.u0 >= w.rbase + r.units) {
       w.rbase += r.units;
       for (++w.ri; w.ri < a.R; w.ri += 32) {
@@ -136,6 +149,7 @@ __device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, int tokens,
         const unsigned busy = __ballot_sync(0xffffffffu, i < a.R && request<KEYS>(a, i, tokens).units > 0);
         if (busy != 0) {
           w.ri += __ffs(busy) - 1;
+          w.r = request<KEYS>(a, w.ri, tokens);
           break;
         }
       }

@@ -12,11 +12,12 @@
 // producer walks the CTA's segments on its own, through a ring of 64-key stages
 // (K and V, 32 KB at head dim 128: 6 stages an SM, 192 KB in flight where some
 // 45 KB cover the latency at full bandwidth), and hands each segment's
-// description and query rows over in a two-slot ring, so that no load waits for
+// description and query rows over in a three-slot ring, so that no load waits for
 // arithmetic and the stages keep filling across segments.  A consumer warp
 // takes 16 of a stage's 64 keys through mma.sync with its own running maximum
 // and sum (fp32): no synchronisation inside a segment but the stages' own
-// barriers.  At its end the four warps join through the last stage's memory.
+// barriers.  At its end the four warps join through the last stage's memory, after
+// one meeting.
 // P is rounded to bf16 for the product with V, its sums are taken before.
 //
 // Rows of V behind the last key may hold anything (stale cache rows): the
@@ -41,15 +42,15 @@ constexpr int kDecThreads = 32 * (kWarps + 1);
 template <int D>
 struct DecCfg {
   static constexpr int NS = D == 128 ? 3 : 6;       // stages
+  static constexpr int NQ = 3;                      // segments handed over
   static constexpr int SLAB = kKeys * 128;          // one 64-column slab of a stage's K or V
   static constexpr int TILE = kKeys * D * 2;        // K or V
   static constexpr int STAGE = 2 * TILE;
   static constexpr int QSLAB = kRows * 128;
   static constexpr int QSLOT = kRows * D * 2;
   static constexpr int OFF_Q = NS * STAGE;
-  static constexpr int SMEM = OFF_Q + 2 * QSLOT + 1024;
-  static constexpr int JROW = D + 4;                // floats of a row in the join
-  static_assert(2 * kRows * JROW * 4 + 4 * kRows * 4 <= STAGE, "the join fits a stage");
+  static constexpr int SMEM = OFF_Q + NQ * QSLOT + 1024;
+  static_assert(kWarps * kRows * D * 4 == STAGE, "the warps' sums fit the rows of their keys");
   static_assert(2 * (SMEM + 2048) <= 233472, "two CTAs an SM");
 };
 
@@ -83,19 +84,22 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     s2_cache_dec_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a) {
   using C = DecCfg<D>;
-  constexpr int NS = C::NS;
+  constexpr int NS = C::NS, NQ = C::NQ;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_qfull[2], bar_qempty[2], bar_join;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_qfull[NQ], bar_qempty[NQ], bar_join;
   __shared__ uint32_t abort_flag;
-  __shared__ long long sums[kDecThreads / 32], found[2];
-  __shared__ Seg segs[2];
+  __shared__ long long sums[kDecThreads / 32];
+  __shared__ Found found;
+  __shared__ Seg segs[NQ];
+  __shared__ float2 stats[2][kWarps][kRows];  // row maxima and sums of the warps, by turns
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   launch_dependents();
+  if (tid < 3) tma_prefetch_desc(tid == 0 ? &tmQ : tid == 1 ? &tmK : &tmV);
   if (tid == 0) a.desc[blockIdx.x] = make_int4(0, -1, 0, 0);
   Run run;
-  if (!locate<kDecThreads, kKeys>(a, a.tpt, kCacheMinUnits, sums, found, run)) return;
+  if (!locate<kDecThreads, kKeys>(a, a.tpt, kCacheMinUnits, sums, &found, run)) return;
   const uint32_t sbase = smem_u32(smem);
   WaitCtx wc{&abort_flag, a.status, a.wait_limit_ns};
   if (tid == 0) {
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       mbar_init(smem_u32(&bar_full[s]), 1);
       mbar_init(smem_u32(&bar_empty[s]), kWarps);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < NQ; ++s) {
       mbar_init(smem_u32(&bar_qfull[s]), 1);
       mbar_init(smem_u32(&bar_qempty[s]), kWarps);
     }
@@ -121,8 +125,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     Seg sg;
     for (;;) {
       const bool more = next_segment<kKeys>(a, a.tpt, run, sg);
-      const int qs = qu & 1;
-      if (qu > 1 && !(ok = warp_wait(smem_u32(&bar_qempty[qs]), ((qu >> 1) - 1) & 1, wc, 140))) break;
+      const int qs = qu % NQ;
+      if (qu >= NQ && !(ok = warp_wait(smem_u32(&bar_qempty[qs]), (qu / NQ - 1) & 1, wc, 140))) break;
       if (lane == 0) {
         if (!more) sg.tiles = -1;
         segs[qs] = sg;
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     if (*wc.abort && lane == 0) {
       // never leave copies in flight into shared memory: wait (bounded) for
       // the last fill of every slot
-      for (int s = 0; s < 2 && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / 2) & 1);
+      for (int s = 0; s < NQ && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / NQ) & 1);
       for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
     }
   } else {
@@ -181,19 +185,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       return warp_wait(smem_u32(&bar_join), nj++ & 1, wc, 144);
     };
     for (int qu = 0;; ++qu) {
-      const int qs = qu & 1;
-      if (!warp_wait(smem_u32(&bar_qfull[qs]), (qu >> 1) & 1, wc, 142)) break;
+      const int qs = qu % NQ;
+      if (!warp_wait(smem_u32(&bar_qfull[qs]), (qu / NQ) & 1, wc, 142)) break;
       const Seg sg = segs[qs];
       if (sg.tiles < 0) break;
-      // ---- Q fragments (rows lane / 4 and lane / 4 + 8), and the slot back
-      uint32_t qf[D / 16][4];
-      if (sg.tiles > 0) {
-        const uint32_t sq = sbase + C::OFF_Q + qs * C::QSLOT;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) ldsm4(qf[k], swz(sq, C::QSLAB, lane & 15, 2 * k + (lane >> 4)));
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_qempty[qs]));
+      const uint32_t sq = sbase + C::OFF_Q + qs * C::QSLOT;
       const int rows = sg.ntok * a.rep;
       float o[D / 8][4];
 #pragma unroll
@@ -206,16 +202,37 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         const uint32_t sk = sbase + s * C::STAGE, sv = sk + C::TILE;
         const int key0 = (sg.kt0 + i) * kKeys + warp * 16;
         if (key0 < sg.keys) {
-          // S = Q K^T for this warp's 16 keys: two n-tiles of 8
-          float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-          const int krow = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+          // S = Q K^T for this warp's 16 keys: two n-tiles of 8, each in two sums.
+          // A warp's latency through a stage is what small calls wait for, so the
+          // fragments are fetched AHEAD steps before the product that takes them
+          // (fetched one by one a stage took 1.3 us), V's first ones before the
+          // softmax.  Q's come from shared memory for every stage: kept in
+          // registers they would not fit beside O at two CTAs an SM.
+          constexpr int AHEAD = 4;
+          float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, sd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          const int krow = warp * 16 + (lane & 7) + ((lane >> 4) << 3), vrow = warp * 16 + (lane & 15);
+          uint32_t fr[AHEAD][4], qf[AHEAD][4];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            ldsm4(fr[k], swz(sk, C::SLAB, krow, 2 * k + ((lane >> 3) & 1)));
+            ldsm4(qf[k], swz(sq, C::QSLAB, lane & 15, 2 * k + (lane >> 4)));
+          }
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            uint32_t b[4];
-            ldsm4(b, swz(sk, C::SLAB, krow, 2 * k + ((lane >> 3) & 1)));
-            mma16816(sc[0], qf[k], b[0], b[1]);
-            mma16816(sc[1], qf[k], b[2], b[3]);
+            uint32_t(&b)[4] = fr[k % AHEAD];
+            mma16816(k & 1 ? sd[0] : sc[0], qf[k % AHEAD], b[0], b[1]);
+            mma16816(k & 1 ? sd[1] : sc[1], qf[k % AHEAD], b[2], b[3]);
+            if (k + AHEAD < D / 16) {
+              ldsm4(b, swz(sk, C::SLAB, krow, 2 * (k + AHEAD) + ((lane >> 3) & 1)));
+              ldsm4(qf[k % AHEAD], swz(sq, C::QSLAB, lane & 15, 2 * (k + AHEAD) + (lane >> 4)));
+            } else {
+              ldsm4t(b, swz(sv, C::SLAB, vrow, 2 * ((k + AHEAD) % (D / 16)) + (lane >> 4)));
+            }
           }
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][e] += sd[n][e];
           if (key0 + 16 > sg.ctx) {  // some key of the warp is a draft or behind the last
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -300,11 +317,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               }
             }
           } else {
-            const int vrow = warp * 16 + (lane & 15);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
-              uint32_t b[4];
-              ldsm4t(b, swz(sv, C::SLAB, vrow, 2 * d + (lane >> 4)));
+              uint32_t(&b)[4] = fr[d % AHEAD];
               if (ragged) {
                 b[0] &= keep[0];
                 b[1] &= keep[1];
@@ -313,6 +328,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               }
               mma16816(o[2 * d], pf, b[0], b[1]);
               mma16816(o[2 * d + 1], pf, b[2], b[3]);
+              if (d + AHEAD < D / 16) ldsm4t(b, swz(sv, C::SLAB, vrow, 2 * (d + AHEAD) + (lane >> 4)));
             }
           }
         }
@@ -320,86 +336,78 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         if (i + 1 < sg.tiles && lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));  // the last stage serves the join first
       }
       if (!ok) break;
-      // ---- join the warps: 2 and 3 into 0 and 1, then 1 into 0, a row per lane quad
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_qempty[qs]));
+      // ---- join the warps.  Each leaves its sums in the last stage, over the K and
+      // V rows of its own 16 keys (which only it reads): 32 columns a slab, the
+      // 16-byte chunks turned by the row as TMA does.  After one meeting all
+      // threads join the four warps' sums, 4 columns of a row each.
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       }
+      float2(&ml)[kWarps][kRows] = stats[nj & 1];  // (segments without a stage do not meet)
+      const uint32_t st = sbase + ((L + NS - 1) % NS) * C::STAGE;
+      auto slab = [&](int p, int w) { return st + (p < D / 64 ? 0 : C::TILE) + p % (D / 64) * C::SLAB + w * 2048; };
       if (sg.tiles > 0) {
-        const int s = (L - 1) % NS;
-        float* jo = reinterpret_cast<float*>(smem + s * C::STAGE);  // [2][row][D + 4]
-        float* jm = jo + 2 * kRows * C::JROW;                       // [2][row] maxima, then sums
-#pragma unroll
-        for (int half = 2; half > 0; half >>= 1) {
-          if (!(ok = meet())) break;  // the stage (or the buffers of the step before) have been read
-          if (warp >= half && warp < 2 * half) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = (lane >> 2) + 8 * h, at = (warp - half) * kRows + row;
-              if (8 * h < rows) {
-#pragma unroll
-                for (int d = 0; d < D / 8; ++d)
-                  *reinterpret_cast<float2*>(jo + at * C::JROW + d * 8 + (lane & 3) * 2) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
-                if ((lane & 3) == 0) {
-                  jm[at] = m[h];
-                  jm[2 * kRows + at] = l[h];
-                }
-              }
-            }
-          }
-          if (!(ok = meet())) break;
-          if (warp < half) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = (lane >> 2) + 8 * h, at = warp * kRows + row;
-              if (8 * h < rows) {
-                const float om = jm[at], mn = fmaxf(m[h], om), fa = ex2_approx(m[h] - mn), fb = ex2_approx(om - mn);
-                m[h] = mn;
-                l[h] = fa * l[h] + fb * jm[2 * kRows + at];
-#pragma unroll
-                for (int d = 0; d < D / 8; ++d) {
-                  const float2 v = *reinterpret_cast<const float2*>(jo + at * C::JROW + d * 8 + (lane & 3) * 2);
-                  o[d][2 * h] = fmaf(fa, o[d][2 * h], fb * v.x);
-                  o[d][2 * h + 1] = fmaf(fa, o[d][2 * h + 1], fb * v.y);
-                }
-              }
-            }
-          }
-        }
-        if (!ok) break;
-        fence_proxy_async_smem();  // these accesses before the TMA that refills the stage
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));
-      }
-      // ---- out: o and lse, or this CTA's part (slot 0: the item began before, 1: it begins here)
-      if (warp == 0) {
-        float* part = Part<kRows, D>::at(a, blockIdx.x, sg.first);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int row = (lane >> 2) + 8 * h;
-          if (row >= rows) continue;
-          if (sg.whole) {
-            const int jt = row / a.rep, head = sg.kvh * a.rep + row - jt * a.rep, tk = sg.row0 + sg.tok + jt;
-            const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
-            __nv_bfloat16* dst = a.o + (static_cast<size_t>(tk) * a.H + head) * D + (lane & 3) * 2;
+          if (8 * h >= rows) continue;
 #pragma unroll
-            for (int d = 0; d < D / 8; ++d)
-              *reinterpret_cast<uint32_t*>(dst + d * 8) = pack_bf16x2(o[d][2 * h] * inv, o[d][2 * h + 1] * inv);
-            if ((lane & 3) == 0) a.lse[static_cast<size_t>(head) * a.T + tk] = lse_of(m[h], l[h]);
-          } else {
+          for (int d = 0; d < D / 8; ++d) {
+            const uint32_t at = slab(d >> 2, warp) + row * 128 + ((((d & 3) * 2 + ((lane & 3) >> 1)) ^ (row & 7)) << 4) + (lane & 1) * 8;
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(o[d][2 * h]), "f"(o[d][2 * h + 1]) : "memory");
+          }
+          if ((lane & 3) == 0) ml[warp][row] = make_float2(m[h], l[h]);
+        }
+        if (!meet()) break;
+      }
+      // ---- out: o and lse, or this CTA's part (slot 0: the item began before, 1: it begins here)
+      float* part = Part<kRows, D>::at(a, blockIdx.x, sg.first);
+      for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
+        const int row = e / (D / 4), c = e % (D / 4);  // columns 4 c .. 4 c + 3
+        float mm = kFloor, ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (sg.tiles > 0) {
 #pragma unroll
-            for (int d = 0; d < D / 8; ++d)
-              *reinterpret_cast<float2*>(part + row * D + d * 8 + (lane & 3) * 2) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
-            if ((lane & 3) == 0) {
-              part[kRows * D + row] = m[h];
-              part[kRows * (D + 1) + row] = l[h];
-            }
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w][row].x);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 x = ml[w][row];
+            if (x.y == 0.f) continue;  // no key of this warp's is seen
+            const float f = ex2_approx(x.x - mm);
+            const float4 v = lds_f4(slab(c >> 3, w) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            ll = fmaf(f, x.y, ll);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
           }
         }
-        if (lane == 0 && sg.first && !sg.whole)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
-          a.desc[blockIdx.x] = join_work(sg);
+        if (sg.whole) {
+          const int jt = row / a.rep, head = sg.kvh * a.rep + row - jt * a.rep, tk = sg.row0 + sg.tok + jt;
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(tk) * a.H + head) * D + 4 * c) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (c == 0) a.lse[static_cast<size_t>(head) * a.T + tk] = lse_of(mm, ll);
+        } else {
+          *reinterpret_cast<float4*>(part + row * D + 4 * c) = acc;
+          if (c == 0) {
+            part[kRows * D + row] = mm;
+            part[kRows * (D + 1) + row] = ll;
+          }
+        }
       }
+      if (sg.tiles > 0) {
+        fence_proxy_async_smem();  // these accesses before the TMA that refills the stage
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_empty[(L + NS - 1) % NS]));
+      }
+      if (tid == 0 && sg.first && !sg.whole)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
+        a.desc[blockIdx.x] = join_work(sg);
     }
   }
 }

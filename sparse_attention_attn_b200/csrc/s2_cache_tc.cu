@@ -77,14 +77,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Seg segs[C::NG];
   __shared__ uint32_t odd[C::NG];  // the segment's drafts hold infinite or NaN values
   __shared__ uint32_t tmem_slot, abort_flag;
-  __shared__ long long sums[kThreads / 32], found[2];
+  __shared__ long long sums[kThreads / 32];
+  __shared__ Found found;
   __shared__ float b_m[kTile], b_l[kTile];  // alternating: warpgroup B's row maxima and sums
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   launch_dependents();
+  if (tid < 3) tma_prefetch_desc(tid == 0 ? &tmQ : tid == 1 ? &tmK : &tmV);
   if (tid == 0) a.desc[blockIdx.x] = make_int4(0, -1, 0, 0);
   Run run;
-  if (!locate<kThreads, kTile>(a, 2 * a.tpt, 1, sums, found, run)) return;
+  if (!locate<kThreads, kTile>(a, 2 * a.tpt, 1, sums, &found, run)) return;
   WaitCtx wc{&abort_flag, a.status, a.wait_limit_ns};
   const uint32_t sQ = smem_u32(smem);
   auto q_addr = [&](int s) { return sQ + s * C::TILE; };
@@ -135,12 +137,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (elect_one()) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
-    __syncwarp();
     Seg sg;
     int qu = 0, L = 0;  // ring uses so far
     bool ok = true;

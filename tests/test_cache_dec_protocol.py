@@ -1,12 +1,13 @@
 """A model of the few-row cache attention kernel's synchronisation
-(csrc/s2_cache_dec.cu), run on the CPU: the TMA producer with its two-slot ring of
+(csrc/s2_cache_dec.cu), run on the CPU: the TMA producer with its three-slot ring of
 segment descriptions and query rows and its ring of K/V stages, the four consumer
-warps, their join through the last stage's memory (two halving steps between
-meetings of the warps) and the copies in flight, interleaved at random with the kernel's
+warps, their join through the last stage's memory (each over its own keys' rows,
+one meeting, then all read all) with the row statistics in buffers used by turns,
+and the copies in flight, interleaved at random with the kernel's
 arrival counts and phases.  It checks that every program finishes, that no parity
 wait is ahead of or overrun by its barrier, that every warp reads the stage and
-the segment it means, that the join's buffers are not written while a warp still
-reads the stage or the step before, and that no stage is refilled in use.  A
+the segment it means, that the join reads what it means and no statistics are
+overwritten in use, and that no stage is refilled in use.  A
 segment is its number of stages; 0: nothing visible."""
 import random
 
@@ -14,28 +15,28 @@ import pytest
 
 from tests.test_cache_attn_protocol import Bar
 
-WARPS = 4
+WARPS, NQ = 4, 3
 
 
-def run(segs, seed, NS=3, release_early=False):
+def run(segs, seed, NS=3, release_early=False, by_segment=False):
     rnd = random.Random(seed)
     bars = {("sync", 0): Bar(WARPS)}
     for s in range(NS):
         bars[("full", s)], bars[("empty", s)] = Bar(1), Bar(WARPS)
-    for s in range(2):
+    for s in range(NQ):
         bars[("qfull", s)], bars[("qempty", s)] = Bar(1), Bar(WARPS)
     err, tma = [], []
     ring, users = [None] * NS, [0] * NS       # stage contents, warps that still need them
-    slot, susers = [None, None], [0, 0]       # segment slots
-    using = {}                                # what a warp reads of the stage its segment ends in
-    sums = {}                                 # what the join's buffers of a stage hold
+    slot, susers = [None] * NQ, [0] * NQ      # segment slots
+    sums, stats = {}, {}                      # what the warps left in a stage, and in the statistics' buffers
+    reading = [None] * WARPS                  # the statistics a warp reads
 
     def producer():
         L = qu = 0
         for k, n in enumerate([*segs, -1]):
-            qs = qu & 1
-            if qu > 1:
-                yield ("wait", ("qempty", qs), (qu >> 1) - 1)
+            qs = qu % NQ
+            if qu >= NQ:
+                yield ("wait", ("qempty", qs), qu // NQ - 1)
             if susers[qs]:
                 err.append("segment slot overwritten")
             slot[qs], susers[qs] = ("in flight" if n > 0 else k), WARPS
@@ -63,15 +64,13 @@ def run(segs, seed, NS=3, release_early=False):
     def consumer(w):
         L = nsync = 0
         for qu, n in enumerate([*segs, -1]):
-            qs = qu & 1
-            yield ("wait", ("qfull", qs), qu >> 1)
+            qs = qu % NQ
+            yield ("wait", ("qfull", qs), qu // NQ)
             if slot[qs] != qu:
                 err.append(f"warp {w} reads segment {slot[qs]} for {qu}")
             if n < 0:
                 return
-            susers[qs] -= 1
-            yield ("arrive", ("qempty", qs))
-            reading = None
+            last = None
             for i in range(n):
                 s = L % NS
                 yield ("wait", ("full", s), L // NS)
@@ -82,36 +81,29 @@ def run(segs, seed, NS=3, release_early=False):
                     users[s] -= 1
                     yield ("arrive", ("empty", s))
                     continue
-                reading = s
-                using[w] = (s, "stage")
+                last = s
                 if release_early:
                     yield ("arrive", ("empty", s))
                 yield ("pause",)
-            if reading is None:
+            susers[qs] -= 1
+            yield ("arrive", ("qempty", qs))
+            if last is None:
                 continue
-            s = reading
-            for half in (2, 1):
-                using.pop(w)             # done with the stage, or with the step before
-                yield ("arrive", ("sync", 0))
-                yield ("wait", ("sync", 0), nsync)
-                nsync += 1
-                using[w] = (s, None)
-                if half <= w < 2 * half:
-                    if any(u in ((s, "stage"), (s, w - half)) for u in using.values()):
-                        err.append(f"join of segment {qu} writes over {using}")
-                    sums[s, w - half] = (qu, w, half)
-                yield ("arrive", ("sync", 0))
-                yield ("wait", ("sync", 0), nsync)
-                nsync += 1
-                if w < half:
-                    using[w] = (s, w)
-                    if sums.get((s, w)) != (qu, w + half, half) or ring[s] != (qu, n - 1):
-                        err.append(f"warp {w} joins {sums.get((s, w))} in {ring[s]}")
-                    yield ("pause",)
-            using.pop(w)
-            users[s] -= 1
+            buf = qu & 1 if by_segment else nsync & 1
+            if any(x == buf for x in reading):
+                err.append(f"statistics of segment {qu} written over those in use")
+            sums[last, w], stats[buf, w] = qu, qu
+            yield ("arrive", ("sync", 0))
+            yield ("wait", ("sync", 0), nsync)
+            nsync += 1
+            reading[w] = buf
+            yield ("pause",)
+            if ring[last] != (qu, n - 1) or any((sums[last, x], stats[buf, x]) != (qu, qu) for x in range(WARPS)):
+                err.append(f"warp {w} joins {sums} {stats} in {ring[last]}")
+            reading[w] = None
+            users[last] -= 1
             if not release_early:
-                yield ("arrive", ("empty", s))
+                yield ("arrive", ("empty", last))
 
     actors = {"producer": producer(), **{f"warp {w}": consumer(w) for w in range(WARPS)}}
     pending, finished = {n: None for n in actors}, set()
@@ -170,3 +162,8 @@ def test_few_row_protocol_runs_clean(NS):
 def test_model_finds_a_stage_released_before_the_join():
     """Releasing the last stage before the join that uses its memory: the check is not vacuous."""
     assert any(run([4, 5, 3], seed, release_early=True) for seed in range(40))
+
+
+def test_model_finds_statistics_buffers_that_do_not_alternate():
+    """Buffers chosen by the segment's number: one without a stage between two others breaks the turns."""
+    assert any(run([2, 0, 1, 0, 1], seed, 6, by_segment=True) for seed in range(200))
