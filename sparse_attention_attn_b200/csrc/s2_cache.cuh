@@ -48,6 +48,12 @@ __device__ __forceinline__ Req request(const CacheAttnArgs& a, int i, int tokens
   return r;
 }
 
+// Keys that the request's first `tokens` new tokens see at most (chains: up to
+// the last one's own).
+__device__ __forceinline__ int visible_keys(const CacheAttnArgs& a, const Req& r, int tokens) {
+  return a.mask != nullptr ? r.keys : min(r.ctx + min(tokens, r.keys - r.ctx), r.keys);
+}
+
 struct Seg {
   int ri, kvh;
   int row0, ctx, keys;  // the request (row0: first row of q)
@@ -166,9 +172,7 @@ __device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, int tokens,
     s.ntok = min(tokens, r.n - s.tok);
     s.kt0 = static_cast<int>(in - item * r.kt);
     const int kt1 = static_cast<int>(min(static_cast<long long>(r.kt), s.kt0 + (w.u1 - w.u0)));
-    // chains: keys behind the item's last token are not visited
-    const int reach = a.mask != nullptr ? r.keys : min(r.ctx + min(s.tok + s.ntok, r.keys - r.ctx), r.keys);
-    s.tiles = max(min(kt1, (reach + KEYS - 1) / KEYS) - s.kt0, 0);
+    s.tiles = max(min(kt1, (visible_keys(a, r, s.tok + s.ntok) + KEYS - 1) / KEYS) - s.kt0, 0);
     s.first = s.kt0 == 0;
     s.whole = s.first && kt1 == r.kt;
     s.last_cta = static_cast<int>((w.rbase + (item + 1) * r.kt - 1) / w.per);

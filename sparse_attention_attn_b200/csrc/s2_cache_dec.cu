@@ -17,8 +17,16 @@
 // takes 16 of a stage's 64 keys through mma.sync with its own running maximum
 // and sum (fp32): no synchronisation inside a segment but the stages' own
 // barriers.  At its end the four warps join through the last stage's memory, after
-// one meeting.
-// P is rounded to bf16 for the product with V, its sums are taken before.
+// one meeting.  P is rounded to bf16 for the product with V, its sums are taken
+// before.
+//
+// A single request takes a form of its own where its grid fills the device (the
+// host's rule has the figures): a cluster of CTAs an item, joined through
+// distributed shared memory.
+//
+// Measured, head dim 128 (bf16): 32 requests of 1K to 32K keys, 64/8 heads, 348 us,
+// 6.8 TB/s, 98% of a copy's rate; one request of 4097 keys, 32/8 heads, 12.3 us
+// (14.4 with the joining launch): latency.
 //
 // Rows of V behind the last key may hold anything (stale cache rows): the
 // fragments that hold them are zeroed in registers.
@@ -79,7 +87,46 @@ __device__ __forceinline__ uint32_t swz(uint32_t base, int slab, int r, int c) {
   return base + (c >> 3) * slab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-template <int D>
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster that have not ended meet; what was written to
+// shared memory before is visible in the cluster after.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of `addr` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// CL: the form for a single request.  All items have the same keys, so each gets
+// a cluster of CTAs with an equal share of the key tiles, and the cluster joins
+// its parts through distributed shared memory: one launch and nothing in the
+// workspace.
+template <int D, bool CL>
 __global__ void __launch_bounds__(kDecThreads, 2)
     s2_cache_dec_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a) {
@@ -94,12 +141,30 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   __shared__ Found found;
   __shared__ Seg segs[NQ];
   __shared__ float2 stats[2][kWarps][kRows];  // row maxima and sums of the warps, by turns
+  __shared__ float2 part_stats[kRows];        // CL: the part's row maxima and sums
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  launch_dependents();
   if (tid < 3) tma_prefetch_desc(tid == 0 ? &tmQ : tid == 1 ? &tmK : &tmV);
-  if (tid == 0) a.desc[blockIdx.x] = make_int4(0, -1, 0, 0);
   Run run;
-  if (!locate<kDecThreads, kKeys>(a, a.tpt, kCacheMinUnits, sums, &found, run)) return;
+  Seg only;  // CL: this CTA's share of its cluster's item
+  if constexpr (CL) {
+    const Req r = request<kKeys>(a, 0, a.tpt);
+    const int item = blockIdx.x / cluster_size(), share = cluster_rank();
+    if (item >= a.Hkv * r.ni) return;  // the whole cluster
+    only.ri = 0;
+    only.kvh = item / r.ni;
+    only.row0 = r.row0, only.ctx = r.ctx, only.keys = r.keys;
+    only.tok = (item - only.kvh * r.ni) * a.tpt;
+    only.ntok = min(a.tpt, r.n - only.tok);
+    const int tiles = (visible_keys(a, r, only.tok + only.ntok) + kKeys - 1) / kKeys;
+    const int per = (tiles + cluster_size() - 1) / cluster_size();
+    only.kt0 = share * per;
+    only.tiles = max(min(per, tiles - only.kt0), 0);
+    only.whole = only.first = only.last_cta = 0;
+  } else {
+    launch_dependents();
+    if (tid == 0) a.desc[blockIdx.x] = make_int4(0, -1, 0, 0);
+    if (!locate<kDecThreads, kKeys>(a, a.tpt, kCacheMinUnits, sums, &found, run)) return;
+  }
   const uint32_t sbase = smem_u32(smem);
   WaitCtx wc{&abort_flag, a.status, a.wait_limit_ns};
   if (tid == 0) {
@@ -124,7 +189,13 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     const int page_log2 = min(a.bs_log2, 6), page_rows = 1 << page_log2;
     Seg sg;
     for (;;) {
-      const bool more = next_segment<kKeys>(a, a.tpt, run, sg);
+      bool more;
+      if constexpr (CL) {
+        more = qu == 0;
+        sg = only;
+      } else {
+        more = next_segment<kKeys>(a, a.tpt, run, sg);
+      }
       const int qs = qu % NQ;
       if (qu >= NQ && !(ok = warp_wait(smem_u32(&bar_qempty[qs]), (qu / NQ - 1) & 1, wc, 140))) break;
       if (lane == 0) {
@@ -387,7 +458,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
             acc.w = fmaf(f, v.w, acc.w);
           }
         }
-        if (sg.whole) {
+        if constexpr (CL) {  // to the cluster: over the query slots that a single segment leaves free
+          st_shared_v4(sbase + C::OFF_Q + C::QSLOT + row * (D * 4) + c * 16, __float_as_uint(acc.x), __float_as_uint(acc.y),
+                       __float_as_uint(acc.z), __float_as_uint(acc.w));
+          if (c == 0) part_stats[row] = make_float2(mm, ll);
+        } else if (sg.whole) {
           const int jt = row / a.rep, head = sg.kvh * a.rep + row - jt * a.rep, tk = sg.row0 + sg.tok + jt;
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
           *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(tk) * a.H + head) * D + 4 * c) =
@@ -406,31 +481,76 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_empty[(L + NS - 1) % NS]));
       }
-      if (tid == 0 && sg.first && !sg.whole)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
+      if (!CL && tid == 0 && sg.first && !sg.whole)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
         a.desc[blockIdx.x] = join_work(sg);
     }
+  }
+  if constexpr (CL) {
+    // A CTA that gave up a wait comes here too: the reads stay in shared memory
+    // of CTAs that have not ended, whatever it holds.
+    static_assert(kRows * D * 4 <= 2 * C::QSLOT, "the part fits the free query slots");
+    cluster_meet();
+    const int rows = only.ntok * a.rep, parts = cluster_size();
+    if (warp < kWarps)
+      for (int e = cluster_rank() * (kWarps * 32) + tid; e < rows * (D / 4); e += parts * (kWarps * 32)) {
+        const int row = e / (D / 4), c = e % (D / 4);
+        const uint32_t sums_at = sbase + C::OFF_Q + C::QSLOT + row * (D * 4) + c * 16, stat_at = smem_u32(&part_stats[row]);
+        float mm = kFloor, ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int p = 0; p < parts; ++p) {
+          const float2 x = ld_peer_f2(peer_addr(stat_at, p));
+          const float4 v = ld_peer_f4(peer_addr(sums_at, p));
+          if (x.y == 0.f) continue;  // no key of this part is seen
+          const float mn = fmaxf(mm, x.x), fo = ex2_approx(mm - mn), f = ex2_approx(x.x - mn);
+          mm = mn;
+          ll = fo * ll + f * x.y;
+          acc.x = fmaf(fo, acc.x, f * v.x);
+          acc.y = fmaf(fo, acc.y, f * v.y);
+          acc.z = fmaf(fo, acc.z, f * v.z);
+          acc.w = fmaf(fo, acc.w, f * v.w);
+        }
+        const int jt = row / a.rep, head = only.kvh * a.rep + row - jt * a.rep, tk = only.row0 + only.tok + jt;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(tk) * a.H + head) * D + 4 * c) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (c == 0) a.lse[static_cast<size_t>(head) * a.T + tk] = lse_of(mm, ll);
+      }
+    cluster_meet();  // no CTA leaves while its memory is read
   }
 }
 
 template <int D>
 cudaError_t dec_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
-                       int grid, cudaStream_t stream) {
-  const cudaError_t ea =
-      cudaFuncSetAttribute(s2_cache_dec_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<D>::SMEM);
-  if (ea != cudaSuccess) return ea;
-  prof_before(stream, kKernelCacheAttn);
-  s2_cache_dec_kernel<D><<<grid, kDecThreads, DecCfg<D>::SMEM, stream>>>(tq, tk, tv, a);
-  const cudaError_t e = cudaGetLastError();
-  prof_after(stream);
+                       int grid, int cluster, cudaStream_t stream) {
+  auto* const kernel = cluster > 1 ? s2_cache_dec_kernel<D, true> : s2_cache_dec_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<D>::SMEM);
+  if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = DecCfg<D>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  prof_before(stream, kKernelCacheAttn);
+  e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, a);
+  prof_after(stream);
+  if (e != cudaSuccess || cluster > 1) return e;
   return launch_join<kRows, kRows, D, 4, 1>(a, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_dec(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
-                             int D, int grid, cudaStream_t stream) {
-  return D == 64 ? dec_launch<64>(tq, tk, tv, a, grid, stream) : dec_launch<128>(tq, tk, tv, a, grid, stream);
+                             int D, int grid, int cluster, cudaStream_t stream) {
+  return D == 64 ? dec_launch<64>(tq, tk, tv, a, grid, cluster, stream)
+                 : dec_launch<128>(tq, tk, tv, a, grid, cluster, stream);
 }
 
 }  // namespace s2

@@ -511,7 +511,7 @@ cudaError_t launch_qknorm_bwd(const QkNormArgs& a, int D, int w_fp32, int num_sm
 cudaError_t launch_cache_append(const CacheAppendArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_plan(const CachePlanArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_dec(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
-                             int D, int grid, cudaStream_t stream);
+                             int D, int grid, int cluster, cudaStream_t stream);
 cudaError_t launch_cache_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
                             int D, int grid, cudaStream_t stream);
 

@@ -210,8 +210,8 @@ Dims make_segment_dims(int B, int H, int Hkv, int N, int Nk, int D, int causal) 
 // that the per-shape selection would not pick.  It starts from the
 // S2ATTN_TILE environment variable and can be replaced at run time by the
 // s2attn_set_tile_override test hook.  Keys: bwd=split_ds|split|fused, ds_slots=N, bwd_qtile=64|128,
-// fwd_order=snake|pairs, fwd_bn=64|128, fwd_kv=N, bwd_stages=N, nf4_stages=4|5, nf4_dq=8|12, cache=dec|tc.  Unknown
-// keys and values are ignored.
+// fwd_order=snake|pairs, fwd_bn=64|128, fwd_kv=N, bwd_stages=N, nf4_stages=4|5, nf4_dq=8|12,
+// cache=dec|cluster|tc.  Unknown keys and values are ignored.
 std::mutex g_override_mu;
 std::string g_override;
 bool g_override_init = false;
@@ -914,7 +914,26 @@ int validate_qknorm(int B, int N, int H, int Hkv, int D, double eps) {
 bool cache_few_rows(int T, int R, int rep) {
   const std::string v = override_value(tile_override(), "cache");
   if (rep > kCacheRows || v == "tc") return false;
-  return v == "dec" || static_cast<long long>(T) * rep <= static_cast<long long>(R) * kCacheRows;
+  return v == "dec" || v == "cluster" || static_cast<long long>(T) * rep <= static_cast<long long>(R) * kCacheRows;
+}
+
+// CTAs of the cluster that takes an item of a single request of at most `keys`
+// keys (1: no clusters, equal runs over all CTAs and a joining launch).  A
+// cluster saves the joining launch and the table of work, but its grid leaves
+// CTAs idle, as more than 8 clusters of 16 or 32 of 8 are not resident together.
+// Measured, us a call with clusters / without, D = 128: 8 items of 1000 keys
+// 8.4 / 11.5, 4097 12.3 / 14.4, 16000 22.5 / 24.7, 60000 55 / 54 (16 CTAs an
+// item); 16 of 8000 20.5 / 23.1, 60000 97 / 87; 24 of 60000 115 / 122; 32 of
+// 1000 9.3 / 12.3, 100000 239 / 256; 36 of 1000 14.4 / 12.3 (8 CTAs an item).
+// So: the largest cluster whose grid is resident, where a CTA's share is at
+// most 1024 keys, or at any length where the grid is nearly full.
+int cache_cluster(int R, long long items, long long keys, int sms) {
+  const std::string v = override_value(tile_override(), "cache");
+  if (R != 1 || v == "dec") return 1;
+  const int cluster = items <= 8 ? 16 : 8;
+  if (v == "cluster") return items < (1 << 20) ? cluster : 1;
+  if (sms < kCacheSms || items > 32) return 1;
+  return keys <= 1024 * cluster || items >= 24 ? cluster : 1;
 }
 
 QkNormArgs qknorm_args(const void* q, const void* k, const void* w_q, const void* w_k, const float* table, void* yq,
@@ -1221,9 +1240,12 @@ int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, c
       !make_map(&tv, v_cache, 1, num_blocks * block_size, Hkv, D, rows))
     return S2ATTN_ERR_CUDA;
   const int sms = info.sms < kCacheSms ? info.sms : kCacheSms, grid = few ? 2 * sms : sms;
-  const cudaError_t e = few ? launch_cache_dec(tq, tk, tv, a, D, grid, static_cast<cudaStream_t>(stream))
-                            : launch_cache_tc(tq, tk, tv, a, D, grid, static_cast<cudaStream_t>(stream));
-  return launched(e, 2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!few) return launched(launch_cache_tc(tq, tk, tv, a, D, grid, s), 2);
+  const int items = Hkv * ((T + a.tpt - 1) / a.tpt);
+  const int cluster = cache_cluster(R, items, static_cast<long long>(max_blocks) * block_size, info.sms);
+  if (cluster > 1) return launched(launch_cache_dec(tq, tk, tv, a, D, items * cluster, cluster, s), 1);
+  return launched(launch_cache_dec(tq, tk, tv, a, D, grid, 1, s), 2);
 }
 
 size_t s2attn_hga_bwd_workspace_bytes(int B, int H, int Hkv, int N, int D, int G) {

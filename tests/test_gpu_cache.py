@@ -100,7 +100,7 @@ def test_plan_odd_lengths_and_parents():
 
 # ------------------------------------------------------------------ attention
 
-@pytest.fixture(params=["dec", "tc"])
+@pytest.fixture(params=["cluster", "dec", "tc"])
 def kernel(request):
     """Both attention kernels, whichever the call's sizes would pick."""
     from sparse_attention_attn_b200 import _lib
@@ -192,6 +192,24 @@ def test_chain_attention_against_oracle(kernel, lens, H, Hkv, D, bs):
     assert s2().device_status() == 0
     t = _check(b, o, l)
     assert (o[t:] == 5.0).all() and (l[:, t:] == 9.0).all()  # rows of no request as they were
+
+
+@pytest.mark.parametrize("pages", [0, 600, 1100])  # wide tables: the host knows no lengths, only their limit
+@pytest.mark.parametrize("H,Hkv,D", [(8, 8, 64), (9, 9, 128), (24, 24, 128), (33, 33, 64), (16, 1, 128), (24, 8, 128)])
+@pytest.mark.parametrize("ctx,new,tree", [(0, 0, False), (0, 1, False), (63, 1, False), (64, 1, True), (1023, 2, False), (1030, 2, True), (2600, 1, False)])
+def test_single_request(ctx, new, tree, H, Hkv, D, pages):
+    """Whichever form the sizes pick, twice the same bits, rows behind left as they were."""
+    b = _batch([(ctx, new)], H, Hkv, D, 16, _tree_masks([(ctx, new)], 4) if tree else None, 23, pad=0 if new else 2)
+    b["tab"] = np.pad(b["tab"], ((0, 0), (0, max(0, pages - b["tab"].shape[1]))), constant_values=-1)
+    outs = []
+    for _ in range(2):
+        out = torch.full((b["T"], H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        outs.append(_call(b, out=out, lse=torch.full((H, b["T"]), 9.0, device="cuda")))
+    torch.cuda.synchronize()
+    assert s2().device_status() == 0
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    t = _check(b, *outs[0])
+    assert (outs[0][0][t:] == 5.0).all() and (outs[0][1][:, t:] == 9.0).all()
 
 
 @pytest.mark.parametrize("H,Hkv,D,bs", [(40, 1, 64, 16), (128, 1, 128, 64)])
