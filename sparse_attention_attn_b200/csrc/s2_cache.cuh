@@ -6,7 +6,10 @@
 // kv head) against all of the request's keys; a unit is one key tile of an
 // item.  All units of a batch are numbered request by request and dealt to the
 // CTAs in equal contiguous runs, so that a batch of very different lengths, or
-// one long request, loads every SM alike.  A segment is the part of an item
+// one long request, loads every SM alike.  `side` CTAs in a row work side by side:
+// each takes the same run of another kv head, so that what they read at a time
+// lies together in the cache (64 requests of 333 to 16384 keys, 8 kv heads: 342 us
+// with all 8 side by side, 349 one by one).  A segment is the part of an item
 // that lies in one CTA's run.  A segment that is not the whole item leaves
 // unnormalised sums, row maxima and row sums in the workspace, and the join
 // kernel adds the parts in order.  The split depends on the lengths and the SM
@@ -30,7 +33,7 @@ struct Req {
   int ctx, n, row0;  // cached tokens, new tokens, first row of q
   int keys;          // keys in all
   int kt, ni;        // key tiles, items a kv head
-  long long units;   // Hkv * ni * kt
+  long long units;   // Hkv / side * ni * kt
 };
 // KEYS: keys of a tile; tokens: new tokens of an item.
 template <int KEYS>
@@ -44,7 +47,7 @@ __device__ __forceinline__ Req request(const CacheAttnArgs& a, int i, int tokens
   r.keys = static_cast<int>(min(static_cast<long long>(r.ctx) + r.n, most));
   r.kt = (r.keys + KEYS - 1) / KEYS;
   r.ni = (r.n + tokens - 1) / tokens;
-  r.units = static_cast<long long>(a.Hkv) * r.ni * r.kt;
+  r.units = static_cast<long long>(a.Hkv / a.side) * r.ni * r.kt;
   return r;
 }
 
@@ -113,8 +116,9 @@ __device__ __forceinline__ bool locate(const CacheAttnArgs& a, int tokens, int m
     at = total + scan(mine, all);
     total += all;
   }
-  run.per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_units));
-  run.u0 = run.per * blockIdx.x;
+  const int runs = gridDim.x / a.side;
+  run.per = max((total + runs - 1) / runs, static_cast<long long>(min_units));
+  run.u0 = run.per * (blockIdx.x / a.side);
   run.u1 = min(run.u0 + run.per, total);
   if (run.u0 >= run.u1) return false;
   if (tid == 0) found->ri = a.R;
@@ -161,10 +165,10 @@ __device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, int tokens,
       }
       continue;
     }
-    const long long in = w.u0 - w.rbase, item = in / r.kt;  // item = kvh * ni + item of the kv head
-    const int e = static_cast<int>(item % r.ni);
+    const long long in = w.u0 - w.rbase, item = in / r.kt;  // item = kvh / side * ni + item of the kv head
+    const int e = static_cast<int>(item % r.ni), mate = blockIdx.x % a.side;
     s.ri = w.ri;
-    s.kvh = static_cast<int>(item / r.ni);
+    s.kvh = static_cast<int>(item / r.ni) * a.side + mate;
     s.row0 = r.row0;
     s.ctx = r.ctx;
     s.keys = r.keys;
@@ -175,7 +179,7 @@ __device__ __forceinline__ bool next_segment(const CacheAttnArgs& a, int tokens,
     s.tiles = max(min(kt1, (visible_keys(a, r, s.tok + s.ntok) + KEYS - 1) / KEYS) - s.kt0, 0);
     s.first = s.kt0 == 0;
     s.whole = s.first && kt1 == r.kt;
-    s.last_cta = static_cast<int>((w.rbase + (item + 1) * r.kt - 1) / w.per);
+    s.last_cta = static_cast<int>((w.rbase + (item + 1) * r.kt - 1) / w.per) * a.side + mate;
     w.u0 += kt1 - s.kt0;
     return true;
   }
@@ -326,10 +330,11 @@ __global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a) {
   const int4 d = a.desc[blockIdx.x];
   if (d.y < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
-  const int first = blockIdx.x, parts = d.w - first + 1;
+  const int first = blockIdx.x, parts = (d.w - first) / a.side + 1;
   const int row0 = (blockIdx.y * (8 / WPR) + warp / WPR) * RPW;
-  if (WPR == 1 && (row0 / TILE) * a.tpt + (row0 % TILE) / a.rep >= d.y) return;  // rows behind the item's
-  auto part = [&](int p) { return Part<ROWS, D>::at(a, first + p, p == 0 ? 1 : 0); };
+  const int lead = WPR == 1 ? row0 : blockIdx.y * (8 / WPR) * RPW;  // warps that share rows leave together
+  if ((lead / TILE) * a.tpt + (lead % TILE) / a.rep >= d.y) return;  // rows behind the item's
+  auto part = [&](int p) { return Part<ROWS, D>::at(a, first + p * a.side, p == 0 ? 1 : 0); };
   float m[RPW], l[RPW], acc[RPW][PER];
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
@@ -425,8 +430,10 @@ __global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a) {
 template <int ROWS, int TILE, int D, int WPR, int RPW>
 cudaError_t launch_join(const CacheAttnArgs& a, int grid, cudaStream_t stream) {
   prof_before(stream, kKernelCacheMerge);
-  const cudaError_t e =
-      launch_dependent(s2_cache_join_kernel<ROWS, TILE, D, WPR, RPW>, dim3(grid, ROWS * WPR / (8 * RPW)), 256, stream, a);
+  // rows that an item can have, in blocks of 8 / WPR * RPW
+  const int most = ROWS == TILE && a.T < a.tpt ? a.T * a.rep : ROWS, per = 8 / WPR * RPW;
+  const cudaError_t e = launch_dependent(s2_cache_join_kernel<ROWS, TILE, D, WPR, RPW>,
+                                         dim3(grid, (most + per - 1) / per), 256, stream, a);
   prof_after(stream);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -20,13 +20,13 @@
 // one meeting.  P is rounded to bf16 for the product with V, its sums are taken
 // before.
 //
-// A single request takes a form of its own where its grid fills the device (the
-// host's rule has the figures): a cluster of CTAs an item, joined through
-// distributed shared memory.
+// A call with few items and short tables takes a form of its own (the host's rule
+// has the figures): a cluster of CTAs an item, joined through distributed shared
+// memory.
 //
-// Measured, head dim 128 (bf16): 32 requests of 1K to 32K keys, 64/8 heads, 348 us,
-// 6.8 TB/s, 98% of a copy's rate; one request of 4097 keys, 32/8 heads, 12.3 us
-// (14.4 with the joining launch): latency.
+// Measured, head dim 128 (bf16): 64 requests of 333 to 16384 keys, 32/8 heads,
+// 334 us, 6.65 TB/s, what a copy reaches; one request of 4097 keys, 32/8 heads,
+// 12.3 us (14.6 without clusters): latency.
 //
 // Rows of V behind the last key may hold anything (stale cache rows): the
 // fragments that hold them are zeroed in registers.
@@ -122,10 +122,38 @@ __device__ __forceinline__ float2 ld_peer_f2(uint32_t addr) {
   return v;
 }
 
-// CL: the form for a single request.  All items have the same keys, so each gets
-// a cluster of CTAs with an equal share of the key tiles, and the cluster joins
-// its parts through distributed shared memory: one launch and nothing in the
-// workspace.
+// The request and the new tokens of row tile `at`, the requests' row tiles being
+// counted in order; false if there are fewer.  Each warp looks for itself.
+__device__ __forceinline__ bool find_item(const CacheAttnArgs& a, int at, Req& r, Seg& s) {
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < a.R; base += 32) {
+    Req mine = {};
+    if (base + lane < a.R) mine = request<kKeys>(a, base + lane, a.tpt);
+    int end = mine.ni;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, end, m);
+      if (lane >= m) end += o;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, at < end);
+    if (past != 0) {
+      const int l = __ffs(past) - 1;
+      s.ri = base + l;
+      s.row0 = r.row0 = __shfl_sync(0xffffffffu, mine.row0, l);
+      s.ctx = r.ctx = __shfl_sync(0xffffffffu, mine.ctx, l);
+      s.keys = r.keys = __shfl_sync(0xffffffffu, mine.keys, l);
+      s.tok = (at - __shfl_sync(0xffffffffu, end - mine.ni, l)) * a.tpt;
+      s.ntok = min(a.tpt, __shfl_sync(0xffffffffu, mine.n, l) - s.tok);
+      return true;
+    }
+    at -= __shfl_sync(0xffffffffu, end, 31);
+  }
+  return false;
+}
+
+// CL: the form for few items.  Each gets a cluster of CTAs (one or more) with an
+// equal share of its key tiles, which joins its parts through distributed shared
+// memory: one launch, no table of work and nothing in the workspace.
 template <int D, bool CL>
 __global__ void __launch_bounds__(kDecThreads, 2)
     s2_cache_dec_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -147,14 +175,10 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   Run run;
   Seg only;  // CL: this CTA's share of its cluster's item
   if constexpr (CL) {
-    const Req r = request<kKeys>(a, 0, a.tpt);
     const int item = blockIdx.x / cluster_size(), share = cluster_rank();
-    if (item >= a.Hkv * r.ni) return;  // the whole cluster
-    only.ri = 0;
-    only.kvh = item / r.ni;
-    only.row0 = r.row0, only.ctx = r.ctx, only.keys = r.keys;
-    only.tok = (item - only.kvh * r.ni) * a.tpt;
-    only.ntok = min(a.tpt, r.n - only.tok);
+    Req r;
+    if (!find_item(a, item / a.Hkv, r, only)) return;  // the whole cluster
+    only.kvh = item % a.Hkv;
     const int tiles = (visible_keys(a, r, only.tok + only.ntok) + kKeys - 1) / kKeys;
     const int per = (tiles + cluster_size() - 1) / cluster_size();
     only.kt0 = share * per;
@@ -523,7 +547,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 template <int D>
 cudaError_t dec_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
                        int grid, int cluster, cudaStream_t stream) {
-  auto* const kernel = cluster > 1 ? s2_cache_dec_kernel<D, true> : s2_cache_dec_kernel<D, false>;
+  auto* const kernel = cluster > 0 ? s2_cache_dec_kernel<D, true> : s2_cache_dec_kernel<D, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<D>::SMEM);
   if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -541,7 +565,7 @@ cudaError_t dec_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   prof_before(stream, kKernelCacheAttn);
   e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, a);
   prof_after(stream);
-  if (e != cudaSuccess || cluster > 1) return e;
+  if (e != cudaSuccess || cluster > 0) return e;
   return launch_join<kRows, kRows, D, 4, 1>(a, grid, stream);
 }
 

@@ -498,6 +498,7 @@ struct CacheAttnArgs {
   float* partial;                                   // [2 grid][rows (D + 2)]
   int T, R, H, Hkv, rep, num_blocks, bs_log2, max_blocks;
   int tpt;                                          // tokens of a row tile (16 or 128 rows)
+  int side;                                         // kv heads whose CTAs work side by side (divides Hkv and the grid)
   float scale_log2;
   uint32_t* status;
   unsigned long long wait_limit_ns;

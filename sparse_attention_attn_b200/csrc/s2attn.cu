@@ -8,10 +8,12 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
+#include <numeric>
 #include <string>
 #include <vector>
 
@@ -917,23 +919,29 @@ bool cache_few_rows(int T, int R, int rep) {
   return v == "dec" || v == "cluster" || static_cast<long long>(T) * rep <= static_cast<long long>(R) * kCacheRows;
 }
 
-// CTAs of the cluster that takes an item of a single request of at most `keys`
-// keys (1: no clusters, equal runs over all CTAs and a joining launch).  A
-// cluster saves the joining launch and the table of work, but its grid leaves
-// CTAs idle, as more than 8 clusters of 16 or 32 of 8 are not resident together.
-// Measured, us a call with clusters / without, D = 128: 8 items of 1000 keys
-// 8.4 / 11.5, 4097 12.3 / 14.4, 16000 22.5 / 24.7, 60000 55 / 54 (16 CTAs an
-// item); 16 of 8000 20.5 / 23.1, 60000 97 / 87; 24 of 60000 115 / 122; 32 of
-// 1000 9.3 / 12.3, 100000 239 / 256; 36 of 1000 14.4 / 12.3 (8 CTAs an item).
-// So: the largest cluster whose grid is resident, where a CTA's share is at
-// most 1024 keys, or at any length where the grid is nearly full.
+// CTAs of the cluster that takes an item of a call with few rows (0: no
+// clusters, equal runs over all CTAs and a joining launch), from the number of
+// items and of keys that a request can have.  A cluster saves the joining launch
+// and the table of work, and its CTAs begin at once; but an item's CTAs get no
+// help from others, which a batch of very different lengths pays for, and no more
+// than 8 clusters of 16, 32 of 8 or 256 CTAs in all are resident together.
+// Measured, us a call with clusters / without, 32 query and 8 kv heads of 128,
+// requests x keys: 1 x 1000 8.4 / 12.3 (16 CTAs an item), 1 x 4000 12.3 / 14.4,
+// 1 x 16000 22.5 / 24.7, 1 x 60000 55 / 54; 4 x 1000 10.3 / 12.9 (8), 4 x 2000
+// 12.3 / 14.5; 8 x 2000 18.9 / 22.7 (4), 8 x 200..4000 22.8 / 24.5; 16 x 2000
+// 28.8 / 34.6 (2), 16 x 200..4000 33.7 / 35.4; 32 x 1000 27.6 / 34.4 (1), 32 x
+// 200..4000 58 / 56; 64 x 500..1000 43 / 45 (1), 64 x 200..4000 105 / 97.  One
+// request, as many query as kv heads, 8 CTAs an item: 24 heads x 60000 keys
+// 115 / 122, 32 x 100000 239 / 256, 36 x 1000 14.4 / 12.3.
+// So: the largest cluster whose grid is resident (beyond, one CTA an item, up to
+// two waves), where a CTA's share is at most 1024 keys, or at any length where one
+// request nearly fills the grid.  Each CTA scans the requests on its own: few.
 int cache_cluster(int R, long long items, long long keys, int sms) {
   const std::string v = override_value(tile_override(), "cache");
-  if (R != 1 || v == "dec") return 1;
-  const int cluster = items <= 8 ? 16 : 8;
-  if (v == "cluster") return items < (1 << 20) ? cluster : 1;
-  if (sms < kCacheSms || items > 32) return 1;
-  return keys <= 1024 * cluster || items >= 24 ? cluster : 1;
+  const int c = items <= 8 ? 16 : items <= 32 ? 8 : items <= 64 ? 4 : items <= 128 ? 2 : 1;
+  if (v == "cluster") return items < (1 << 20) ? c : 0;
+  if (v == "dec" || sms < kCacheSms || R > 128 || items > 4 * kCacheSms) return 0;
+  return keys <= 1024 * c || (R == 1 && items * c >= 192 && items * c <= 256) ? c : 0;
 }
 
 QkNormArgs qknorm_args(const void* q, const void* k, const void* w_q, const void* w_k, const float* table, void* yq,
@@ -1240,12 +1248,15 @@ int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, c
       !make_map(&tv, v_cache, 1, num_blocks * block_size, Hkv, D, rows))
     return S2ATTN_ERR_CUDA;
   const int sms = info.sms < kCacheSms ? info.sms : kCacheSms, grid = few ? 2 * sms : sms;
+  a.side = std::gcd(Hkv, grid);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!few) return launched(launch_cache_tc(tq, tk, tv, a, D, grid, s), 2);
-  const int items = Hkv * ((T + a.tpt - 1) / a.tpt);
-  const int cluster = cache_cluster(R, items, static_cast<long long>(max_blocks) * block_size, info.sms);
-  if (cluster > 1) return launched(launch_cache_dec(tq, tk, tv, a, D, items * cluster, cluster, s), 1);
-  return launched(launch_cache_dec(tq, tk, tv, a, D, grid, 1, s), 2);
+  // row tiles the requests can have in all
+  const int tiles = static_cast<int>((T + static_cast<long long>(std::min(R, T)) * (a.tpt - 1)) / a.tpt);
+  const int cluster = cache_cluster(R, static_cast<long long>(Hkv) * tiles,
+                                    static_cast<long long>(max_blocks) * block_size, info.sms);
+  if (cluster > 0) return launched(launch_cache_dec(tq, tk, tv, a, D, Hkv * tiles * cluster, cluster, s), 1);
+  return launched(launch_cache_dec(tq, tk, tv, a, D, grid, 0, s), 2);
 }
 
 size_t s2attn_hga_bwd_workspace_bytes(int B, int H, int Hkv, int N, int D, int G) {

@@ -56,9 +56,12 @@ class _Without:
         return lambda *args: None
 
 
+def _copies(a):
+    return [x.clone() if isinstance(x, torch.Tensor) else x for x in a]
+
+
 def _public(name, a):
-    """The public call with these operands, and every tensor it returns or writes."""
-    a = [x.clone() if isinstance(x, torch.Tensor) else x for x in a]
+    """The public call with these operands: every tensor it returns or writes."""
     if name == "qknorm_fwd":
         return s2.qknorm_rope_forward(*a)
     if name == "qknorm_bwd":
@@ -74,10 +77,10 @@ def _public(name, a):
 @pytest.mark.parametrize("name", NAMES)
 def test_same_bits_both_ways(fast, monkeypatch, name):
     args = _args("cuda")[name]
-    assert fast[name](*[x.clone() if isinstance(x, torch.Tensor) else x for x in args]) is not None
-    got = _public(name, args)
+    assert fast[name](*_copies(args)) is not None
+    got = _public(name, _copies(args))
     monkeypatch.setattr(api, "_fast", _Without())
-    want = _public(name, args)
+    want = _public(name, _copies(args))
     torch.cuda.synchronize()
     assert s2.device_status() == 0
     for x, y in zip(got, want, strict=True):
@@ -96,6 +99,6 @@ def test_wrong_operands_are_refused_by_name(fast, name):
         for bad in (t.to(torch.float16), t.cpu(), t[None], wide, t.cpu().numpy() if t.dtype != torch.bfloat16 else 1):
             a = [*good]
             a[i] = bad
-            assert fast[name](*a) is None, (i, bad)
+            assert fast[name](*a) is None, (i, str(bad)[:200])
             with pytest.raises((ValueError, TypeError, AttributeError, _lib.S2AttnError)):
                 _public(name, a)
