@@ -116,7 +116,7 @@ def build_binding(force: bool = False):
         return None
     cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I" + INCLUDE, "-I" + python_h,
            "-I" + torch_h, "-I" + os.path.join(torch_h, "torch", "csrc", "api", "include"), "-I" + cuda_h, BINDING_SOURCE,
-           "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     h = hashlib.sha256(" ".join(cmd).encode() + sys.version.encode())
     for f in (BINDING_SOURCE, os.path.join(INCLUDE, "s2attn.h"), version):
         with open(f, "rb") as fh:

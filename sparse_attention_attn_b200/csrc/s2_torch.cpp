@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -96,6 +97,21 @@ T* ptr(const at::Tensor* t) {
   return t == nullptr ? nullptr : static_cast<T*>(t->data_ptr());
 }
 
+// A new contiguous tensor, straight from the allocator: through the dispatcher each
+// costs some 0.2 us more, and a narrowed view 0.8 us (a plan of 64 requests 5.1 us
+// a call, 8.6 with them).
+at::Tensor fresh_tensor(at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
+}
+
+// `n` values of a one-dimensional tensor from `from` on: a tensor on the same memory.
+at::Tensor piece(const at::Tensor& t, int64_t from, int64_t n) {
+  at::Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+  p.unsafeGetTensorImpl()->set_storage_offset(from);
+  p.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return p;
+}
+
 PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
   PyObject* out = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
   if (out == nullptr) return nullptr;
@@ -117,7 +133,7 @@ PyObject* qknorm_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!small(Hkv) || w32 < 0 || !fits(q, at::kBFloat16, {B, N, H, D}, dev) ||
       !fits(k, at::kBFloat16, {B, N, Hkv, D}, dev) || !fits(plain(args[4]), at::kFloat, {N, D / 2, 2}, dev))
     Py_RETURN_NONE;
-  at::Tensor yq = at::empty(q->sizes(), q->options()), yk = at::empty(k->sizes(), k->options());
+  at::Tensor yq = fresh_tensor(q->sizes(), at::kBFloat16, dev), yk = fresh_tensor(k->sizes(), at::kBFloat16, dev);
   const float* table = ptr<float>(plain(args[4]));
   void* s = stream_of(*q);
   const int st = released([&] {
@@ -145,9 +161,9 @@ PyObject* qknorm_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NONE;
   const size_t ws = calls.norm_ws(static_cast<int>(D));
   if (ws == 0) Py_RETURN_NONE;
-  at::Tensor dq = at::empty(q->sizes(), q->options()), dk = at::empty(k->sizes(), k->options());
-  at::Tensor dwq = at::empty({D}, wq->options()), dwk = at::empty({D}, wq->options());
-  at::Tensor work = at::empty({static_cast<int64_t>(ws)}, q->options().dtype(at::kByte));
+  at::Tensor dq = fresh_tensor(q->sizes(), at::kBFloat16, dev), dk = fresh_tensor(k->sizes(), at::kBFloat16, dev);
+  at::Tensor dwq = fresh_tensor({D}, wq->scalar_type(), dev), dwk = fresh_tensor({D}, wq->scalar_type(), dev);
+  at::Tensor work = fresh_tensor({static_cast<int64_t>(ws)}, at::kByte, dev);
   void* s = stream_of(*q);
   const int st = released([&] {
     return calls.norm_bwd(ptr(*q), ptr(*k), ptr(*wq), ptr(*wk), ptr<float>(*table), ptr(*gq), ptr(*gk), ptr(dq), ptr(dk),
@@ -180,7 +196,7 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
       !fits(vc, at::kBFloat16, {nb, bs, Hkv, D}, dev) ||
       (!fresh && !fits(plain(args[11]), at::kBFloat16, {T, H, D}, dev)))
     Py_RETURN_NONE;
-  at::Tensor out = fresh ? at::empty(q->sizes(), q->options()) : *plain(args[11]);
+  at::Tensor out = fresh ? fresh_tensor(q->sizes(), at::kBFloat16, dev) : *plain(args[11]);
   const void* wq = norm ? ptr(plain(args[8])) : nullptr;
   const void* wk = norm ? ptr(plain(args[9])) : nullptr;
   void* s = stream_of(*q);
@@ -215,8 +231,8 @@ PyObject* cache_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
       !fits(tab, at::kInt, {R, width}, dev) || !fits(free_, at::kInt, {nf}, dev) ||
       (tree && !fits(par, at::kInt, {T}, dev)))
     Py_RETURN_NONE;
-  at::Tensor buf = at::empty({2 * T + R + 5}, ctx->options()), mask;  // one allocation for the int32 outputs
-  if (tree) mask = at::empty({T}, ctx->options().dtype(at::kLong));
+  at::Tensor buf = fresh_tensor({2 * T + R + 5}, at::kInt, dev), mask;  // one allocation for the int32 outputs
+  if (tree) mask = fresh_tensor({T}, at::kLong, dev);
   int* p = ptr<int>(buf);
   void* s = stream_of(*ctx);
   const int st = released([&] {
@@ -226,16 +242,16 @@ PyObject* cache_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (st != S2ATTN_OK) Py_RETURN_NONE;
   PyObject* out = PyTuple_New(5);
   if (out == nullptr) return nullptr;
-  PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(buf.narrow(0, 2 * T, R + 1)));
-  PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(buf.narrow(0, 0, T)));
-  PyTuple_SET_ITEM(out, 2, THPVariable_Wrap(buf.narrow(0, T, T)));
+  PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(piece(buf, 2 * T, R + 1)));
+  PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(piece(buf, 0, T)));
+  PyTuple_SET_ITEM(out, 2, THPVariable_Wrap(piece(buf, T, T)));
   if (tree) {
     PyTuple_SET_ITEM(out, 3, THPVariable_Wrap(mask));
   } else {
     Py_INCREF(Py_None);
     PyTuple_SET_ITEM(out, 3, Py_None);
   }
-  PyTuple_SET_ITEM(out, 4, THPVariable_Wrap(buf.narrow(0, 2 * T + R + 1, 4)));
+  PyTuple_SET_ITEM(out, 4, THPVariable_Wrap(piece(buf, 2 * T + R + 1, 4)));
   return out;
   END_HANDLE_TH_ERRORS
 }
@@ -259,8 +275,8 @@ PyObject* cache_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NONE;
   const size_t ws = calls.attn_ws(static_cast<int>(D));
   if (ws == 0) Py_RETURN_NONE;
-  at::Tensor o = at::empty(q->sizes(), q->options()), lse = at::empty({H, T}, q->options().dtype(at::kFloat));
-  at::Tensor work = at::empty({static_cast<int64_t>(ws)}, q->options().dtype(at::kByte));
+  at::Tensor o = fresh_tensor(q->sizes(), at::kBFloat16, dev), lse = fresh_tensor({H, T}, at::kFloat, dev);
+  at::Tensor work = fresh_tensor({static_cast<int64_t>(ws)}, at::kByte, dev);
   const int *ctx = ptr<int>(plain(args[4])), *cu = ptr<int>(plain(args[5]));
   void* s = stream_of(*q);
   const int st = released([&] {
