@@ -416,8 +416,9 @@ S2ATTN_API size_t s2attn_cache_attn_workspace_bytes(int D);
  * D in {64, 128}; H / Hkv <= 128; block_size a power of two from 16 to 256; T H <= 2^30;
  * num_blocks * block_size below 2^31, max_blocks * block_size at most 2^31 - 65536.
  * workspace: 16-byte aligned, s2attn_cache_attn_workspace_bytes(D) bytes, need
- * not be cleared; calls that overlap need one each.  Two launches; the result
- * does not depend on timing.
+ * not be cleared; calls that overlap need one each.  One or two launches; the
+ * result does not depend on timing.  cu_seqlens must not descend (of requests
+ * that overlap, some rows may be left as they were).
  */
 S2ATTN_API int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_tables,
                                  const int* ctx_lens, const int* cu_seqlens, const int64_t* mask, void* o, float* lse,
@@ -540,8 +541,8 @@ S2ATTN_API int s2attn_plan(int B, int H, int Hkv, int N, int D, int G, int num_s
  * 128, 4/6/8 at 64; with 64-key tiles 8 at head dim 128, 8/12 at 64), bwd_stages=N (dK/dV operand
  * stages: 2-4 at head dim 128, 3-4 at 64; the split path's dQ kernel takes at
  * most 3 at head dim 128), nf4_stages=4|5 and nf4_dq=8|12
- * (pipeline depth and dequantization warps of s2attn_nf4_qkv), cache=dec|tc (the few-row or the 128-row kernel of
- * s2attn_cache_attn; dec exists for H / Hkv <= 16); values that do not exist for a call's head dim
+ * (pipeline depth and dequantization warps of s2attn_nf4_qkv), cache=dec|cluster|tc (the few-row kernel with equal runs or in
+ * clusters, or the 128-row kernel, of s2attn_cache_attn; the first two exist for H / Hkv <= 16); values that do not exist for a call's head dim
  * are ignored.  s2attn_bwd_workspace_bytes answers for the
  * path in force when it is called.  Returns S2ATTN_OK.
  */
