@@ -212,6 +212,21 @@ def test_single_request(ctx, new, tree, H, Hkv, D, pages):
     assert (outs[0][0][t:] == 5.0).all() and (outs[0][1][:, t:] == 9.0).all()
 
 
+@pytest.mark.parametrize("pages", [0, 70, 300])  # up to 1024 keys a CTA in clusters, else equal runs
+@pytest.mark.parametrize("R,H,Hkv,D", [(2, 8, 4, 128), (5, 12, 6, 64), (9, 28, 7, 128), (16, 8, 8, 64), (37, 8, 8, 128), (75, 8, 8, 64), (129, 4, 2, 64)])
+def test_batches_of_few_items(R, H, Hkv, D, pages):
+    """Every size of cluster, ragged lengths with requests that have no new token or several."""
+    lens = [((37 * i) % 900, (1, 1, 0, 2, 1)[i % 5]) for i in range(R)]
+    b = _batch(lens, H, Hkv, D, 16, _tree_masks(lens, 6) if pages == 70 else None, 29, pad=2)
+    b["tab"] = np.pad(b["tab"], ((0, 0), (0, max(0, pages - b["tab"].shape[1]))), constant_values=-1)
+    out = torch.full((b["T"], H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    o, l = _call(b, out=out, lse=torch.full((H, b["T"]), 9.0, device="cuda"))
+    torch.cuda.synchronize()
+    assert s2().device_status() == 0
+    t = _check(b, o, l)
+    assert (o[t:] == 5.0).all() and (l[:, t:] == 9.0).all()
+
+
 @pytest.mark.parametrize("H,Hkv,D,bs", [(40, 1, 64, 16), (128, 1, 128, 64)])
 @pytest.mark.parametrize("lens", ["one", "tile-edges", "ragged", "gaps"])
 def test_more_than_16_heads_a_kv_head(lens, H, Hkv, D, bs):
