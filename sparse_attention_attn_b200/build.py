@@ -100,23 +100,32 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     return lib
 
 
-def build_binding(force: bool = False):
-    """Compile _s2torch.so unless an up-to-date build exists.  Returns its
-    path, or None where a compiler or headers are missing (torch is located, not
-    imported)."""
+def binding_command(source: str, out: str, optimize: str = "-O2"):
+    """The command that compiles a binding source, and torch's version file; (None, None)
+    where a compiler or headers are missing (torch is located, not imported)."""
     spec = importlib.util.find_spec("torch")
     gxx, python_h = shutil.which("g++"), sysconfig.get_paths()["include"]
     cuda_h = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
     if spec is None or spec.origin is None or gxx is None:
-        return None
+        return None, None
     torch_dir = os.path.dirname(spec.origin)
     torch_h, version = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "version.py")
     if not all(map(os.path.exists, (os.path.join(python_h, "Python.h"), os.path.join(torch_h, "ATen", "ATen.h"), version,
                                     os.path.join(cuda_h, "cuda_runtime.h")))):
+        return None, None
+    return [gxx, optimize, "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I" + INCLUDE, "-I" + python_h,
+            "-I" + torch_h, "-I" + os.path.join(torch_h, "torch", "csrc", "api", "include"), "-I" + cuda_h, source,
+            "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+            "-o", out], version
+
+
+def build_binding(force: bool = False):
+    """Compile _s2torch.so unless an up-to-date build exists.  Returns its
+    path, or None where a compiler or headers are missing."""
+    tmp = BINDING + ".tmp"
+    cmd, version = binding_command(BINDING_SOURCE, tmp)
+    if cmd is None:
         return None
-    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I" + INCLUDE, "-I" + python_h,
-           "-I" + torch_h, "-I" + os.path.join(torch_h, "torch", "csrc", "api", "include"), "-I" + cuda_h, BINDING_SOURCE,
-           "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     h = hashlib.sha256(" ".join(cmd).encode() + sys.version.encode())
     for f in (BINDING_SOURCE, os.path.join(INCLUDE, "s2attn.h"), version):
         with open(f, "rb") as fh:
@@ -126,8 +135,7 @@ def build_binding(force: bool = False):
         with open(stamp) as fh:
             if fh.read().strip() == h.hexdigest():
                 return BINDING
-    tmp = BINDING + ".tmp"
-    subprocess.run(cmd + ["-o", tmp], check=True)
+    subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
     with open(stamp, "w") as fh:
         fh.write(h.hexdigest())

@@ -32,8 +32,13 @@ struct Calls {
   decltype(&s2attn_cache_attn_workspace_bytes) attn_ws = nullptr;
 } calls;
 
-// The tensor of a plain torch.Tensor or Parameter, else null (subclasses take the Python path).
-const at::Tensor* plain(PyObject* o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
+// The tensor of a plain torch.Tensor or Parameter, else null (subclasses take the Python path).  A tensor
+// inside torch.vmap or torch.func.grad is of the plain type too, but has no memory of its own: null.
+const at::Tensor* plain(PyObject* o) {
+  if (!THPVariable_CheckExact(o)) return nullptr;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  return t.has_storage() ? &t : nullptr;
+}
 
 bool fits(const at::Tensor* t, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {
   return t != nullptr && t->scalar_type() == type && t->layout() == at::kStrided && t->device() == dev &&
@@ -79,13 +84,15 @@ int weights(const at::Tensor* wq, const at::Tensor* wk, int64_t D, c10::Device d
   return fits(wq, t, {D}, dev) && fits(wk, t, {D}, dev) ? t == at::kFloat : -1;
 }
 
+// f() without the interpreter lock, which is taken back however f ends: an exception reaches the handlers
+// of HANDLE_TH_ERRORS, which use Python.
 template <typename F>
 int released(F f) {
-  int st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f();
-  Py_END_ALLOW_THREADS;
-  return st;
+  struct Release {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Release() { PyEval_RestoreThread(state); }
+  } release;
+  return f();
 }
 
 template <typename T = void>
