@@ -480,6 +480,10 @@ S2ATTN_API int s2attn_selftest_wait_timeout(uint32_t* status_out, uint64_t limit
  */
 S2ATTN_API int s2attn_debug_checks(void);
 
+/* Names the s2attn.h that the library was compiled with (a hash the build script gives; "unknown" without it).
+ * Code that calls the library by address compares it with what it was compiled with itself. */
+S2ATTN_API const char* s2attn_header_hash(void);
+
 /* Number of kernel launches the last s2attn_fwd / s2attn_bwd call made on this host thread. */
 S2ATTN_API int s2attn_last_launch_count(void);
 

@@ -38,6 +38,7 @@ SIGNATURES = {
     "s2attn_selftest_wait_timeout": (_i, [_vp, ctypes.c_uint64, _vp]),
     "s2attn_last_launch_count": (_i, []),
     "s2attn_debug_checks": (_i, []),
+    "s2attn_header_hash": (ctypes.c_char_p, []),
     "s2attn_last_cuda_error": (_i, []),
     "s2attn_cuda_error_string": (ctypes.c_char_p, [_i]),
     "s2attn_profile_start": (_i, [_i]),

@@ -13,6 +13,7 @@ attention.  Training uses the shifted groups, inference the dense path.
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -23,8 +24,10 @@ from . import _lib
 class _Binding:
     """The calls of _s2torch.so (csrc/s2_torch.cpp: the usual case of the smallest
     calls in one step, None for any other), bound at the first use to the library
-    the ctypes binding loaded; where it is not built or does not load, functions
-    that leave every call to the Python path."""
+    the ctypes binding loaded; where it is not built, does not load, or was
+    compiled for another interface of the library or another torch (it calls the
+    one by address and reads the other's tensors by their layout), functions that
+    leave every call to the Python path."""
 
     _NAMES = ("qknorm_fwd", "qknorm_bwd", "cache_append", "cache_plan", "cache_attention")
 
@@ -34,6 +37,12 @@ class _Binding:
         lib = _lib.load()
         try:
             from . import _s2torch
+            ours = (lib.s2attn_header_hash().decode(), f"{torch.version.__version__} {torch.version.git_version}")
+            its = (getattr(_s2torch, "header_hash", None), getattr(_s2torch, "torch_version", None))
+            if its != ours:
+                warnings.warn(f"_s2torch.so was built for {its}, not for {ours}: its calls take the Python way until "
+                              "`python -m sparse_attention_attn_b200.build` is run", RuntimeWarning, stacklevel=3)
+                raise ImportError("_s2torch.so is of another build")
             _s2torch.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
                             ("s2attn_qknorm_rope_fwd", "s2attn_qknorm_rope_bwd",
                              "s2attn_qknorm_rope_bwd_workspace_bytes", "s2attn_cache_append", "s2attn_cache_plan",

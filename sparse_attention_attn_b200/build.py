@@ -17,6 +17,7 @@ from __future__ import annotations
 import hashlib
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -44,6 +45,13 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libs2attn.so")
 
 
+def header_hash() -> str:
+    """Name of the interface in include/s2attn.h; compiled into the library and
+    into _s2torch.so, which calls the library by address."""
+    with open(os.path.join(INCLUDE, "s2attn.h"), "rb") as fh:
+        return "h" + hashlib.sha256(fh.read()).hexdigest()[:16]
+
+
 def source_hash(debug: bool = False) -> str:
     h = hashlib.sha256()
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "s2attn.h")]
@@ -64,9 +72,12 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     compile in parallel."""
     if not debug:
         try:
-            build_binding(force)
+            built = build_binding(force)
+            why = "no compiler or headers for it"
         except (OSError, subprocess.CalledProcessError) as e:
-            print(f"warning: _s2torch.so was not built ({e}); the Python path serves alone", file=sys.stderr)
+            built, why = None, e
+        if built is None:
+            print(f"warning: _s2torch.so was not built ({why}); the Python path serves alone", file=sys.stderr)
     lib = LIB_DEBUG if debug else LIB
     stamp = lib + ".srchash"
     digest = source_hash(debug)
@@ -78,7 +89,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     tmpdir = os.path.join(PKG, "_build_debug" if debug else "_build")
     os.makedirs(tmpdir, exist_ok=True)
     common = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
-                     "-I" + INCLUDE, "-I" + CSRC, "--expt-relaxed-constexpr"]
+                     "-I" + INCLUDE, "-I" + CSRC, "--expt-relaxed-constexpr", "-DS2ATTN_HEADER_HASH=" + header_hash()]
     if debug:
         common += ["-DS2ATTN_DEBUG_CHECKS"]
     if verbose:
@@ -100,41 +111,60 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     return lib
 
 
-def binding_command(source: str, out: str, optimize: str = "-O2"):
-    """The command that compiles a binding source, and torch's version file; (None, None)
-    where a compiler or headers are missing (torch is located, not imported)."""
+BINDING_FLAGS = ["-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"]
+
+
+def _torch_home():
+    """Torch's folder and its version (located and read, not imported); (None, None) without it."""
     spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None, None
+    home = os.path.dirname(spec.origin)
+    try:
+        with open(os.path.join(home, "version.py")) as fh:
+            named = dict(re.findall(r"^(__version__|git_version)\b[^=]*= '([^']*)'", fh.read(), re.M))
+    except OSError:
+        return None, None
+    return home, f"{named.get('__version__')} {named.get('git_version')}"
+
+
+def binding_command(source: str, out: str, optimize: str = "-O2"):
+    """The command that compiles a binding source; None where a compiler or headers are missing."""
     gxx, python_h = shutil.which("g++"), sysconfig.get_paths()["include"]
+    home, version = _torch_home()
+    if home is None or gxx is None:
+        return None
     cuda_h = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
-    if spec is None or spec.origin is None or gxx is None:
-        return None, None
-    torch_dir = os.path.dirname(spec.origin)
-    torch_h, version = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "version.py")
-    if not all(map(os.path.exists, (os.path.join(python_h, "Python.h"), os.path.join(torch_h, "ATen", "ATen.h"), version,
+    torch_h = os.path.join(home, "include")
+    if not all(map(os.path.exists, (os.path.join(python_h, "Python.h"), os.path.join(torch_h, "ATen", "ATen.h"),
                                     os.path.join(cuda_h, "cuda_runtime.h")))):
-        return None, None
-    return [gxx, optimize, "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I" + INCLUDE, "-I" + python_h,
-            "-I" + torch_h, "-I" + os.path.join(torch_h, "torch", "csrc", "api", "include"), "-I" + cuda_h, source,
-            "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
-            "-o", out], version
+        return None
+    return [gxx, optimize, *BINDING_FLAGS, f'-DS2ATTN_HEADER_HASH="{header_hash()}"', f'-DS2TORCH_VERSION="{version}"',
+            "-I" + INCLUDE, "-I" + python_h, "-I" + torch_h,
+            "-I" + os.path.join(torch_h, "torch", "csrc", "api", "include"), "-I" + cuda_h, source,
+            "-L" + os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+            "-o", out]
 
 
 def build_binding(force: bool = False):
     """Compile _s2torch.so unless an up-to-date build exists.  Returns its
-    path, or None where a compiler or headers are missing."""
-    tmp = BINDING + ".tmp"
-    cmd, version = binding_command(BINDING_SOURCE, tmp)
-    if cmd is None:
-        return None
-    h = hashlib.sha256(" ".join(cmd).encode() + sys.version.encode())
-    for f in (BINDING_SOURCE, os.path.join(INCLUDE, "s2attn.h"), version):
-        with open(f, "rb") as fh:
-            h.update(fh.read())
-    stamp = BINDING + ".srchash"
+    path, or None where a compiler or headers are missing.  A build of other
+    sources or for another torch is removed first: it would call the library by
+    an old interface, or read torch's tensors by an old layout."""
+    stamp, tmp = BINDING + ".srchash", BINDING + ".tmp"
+    h = hashlib.sha256(f"{BINDING_FLAGS} {sys.version} {_torch_home()[1]} {header_hash()}".encode())
+    with open(BINDING_SOURCE, "rb") as fh:
+        h.update(fh.read())
     if not force and os.path.exists(BINDING) and os.path.exists(stamp):
         with open(stamp) as fh:
             if fh.read().strip() == h.hexdigest():
                 return BINDING
+    for old in (stamp, BINDING):
+        if os.path.exists(old):
+            os.remove(old)
+    cmd = binding_command(BINDING_SOURCE, tmp)
+    if cmd is None:
+        return None
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
     with open(stamp, "w") as fh:

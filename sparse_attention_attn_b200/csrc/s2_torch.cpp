@@ -326,4 +326,20 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_s2torch", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__s2torch() { return PyModule_Create(&module); }
+// What this was compiled against (the loader compares it with the library and the torch it finds).
+#ifndef S2ATTN_HEADER_HASH
+#define S2ATTN_HEADER_HASH "unknown"
+#endif
+#ifndef S2TORCH_VERSION
+#define S2TORCH_VERSION "unknown"
+#endif
+
+PyMODINIT_FUNC PyInit__s2torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && (PyModule_AddStringConstant(m, "header_hash", S2ATTN_HEADER_HASH) != 0 ||
+                       PyModule_AddStringConstant(m, "torch_version", S2TORCH_VERSION) != 0)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -535,6 +535,16 @@ int s2attn_debug_checks(void) {
 #endif
 }
 
+#define S2ATTN_TEXT_(x) #x
+#define S2ATTN_TEXT(x) S2ATTN_TEXT_(x)
+const char* s2attn_header_hash(void) {
+#ifdef S2ATTN_HEADER_HASH
+  return S2ATTN_TEXT(S2ATTN_HEADER_HASH);
+#else
+  return "unknown";
+#endif
+}
+
 int s2attn_last_cuda_error(void) { return g_last_cuda_error; }
 
 const char* s2attn_cuda_error_string(int err) {

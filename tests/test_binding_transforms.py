@@ -67,7 +67,7 @@ def test_transformed_tensors_are_left_to_python(tmp_path):
     src = src.replace("PyInit__s2torch", "PyInit__relaxed")
     (tmp_path / "relaxed.cpp").write_text(src)
     (tmp_path / "fake.c").write_text("int ok(void) { return 0; }\nunsigned long bytes(void) { return 64; }\n")
-    cmd, _ = build.binding_command(str(tmp_path / "relaxed.cpp"), str(tmp_path / "_relaxed.so"), "-O0")
+    cmd = build.binding_command(str(tmp_path / "relaxed.cpp"), str(tmp_path / "_relaxed.so"), "-O0")
     if cmd is None:
         pytest.skip("no compiler or no torch headers")
     subprocess.run(cmd, check=True)
