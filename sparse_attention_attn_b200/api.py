@@ -581,6 +581,18 @@ def qknorm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, table, eps: float = 1e-
     return dq, dk, dw_q, dw_k
 
 
+def _optional(name: str, t):
+    """Address of an optional operand, None without it.  The C calls take a null
+    address for its absence, so a tensor without memory (inside
+    torch.func.functionalize) is refused."""
+    if t is None:
+        return None
+    p = t.data_ptr()
+    if p == 0 and t.numel() > 0:
+        raise ValueError(f"{name} has no memory")
+    return p
+
+
 def _out(name: str, t, like):
     """The caller's output checked against the tensor it is shaped like, or a new one."""
     if t is None:
@@ -678,7 +690,7 @@ def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, n
     positions, slots, cu_seqlens, counts = buf.split_with_sizes((T, T, R + 1, 4))
     p = buf.data_ptr()
     _run(dev, "s2attn_cache_plan", ctx_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
-         free_blocks.data_ptr(), None if parents is None else parents.data_ptr(), p + 8 * T, p, p + 4 * T, None if
+         free_blocks.data_ptr(), _optional("parents", parents), p + 8 * T, p, p + 4 * T, None if
          mask is None else mask.data_ptr(), p + 4 * (2 * T + R + 1), R, block_tables.shape[1], free_blocks.shape[0],
          int(block_size), T)
     return CachePlan(cu_seqlens, positions, slots, mask, counts)
@@ -725,10 +737,9 @@ def cache_append(q, k, v, table, positions, slots, k_cache, v_cache, w_q=None, w
         raise ValueError("w_q and w_k go together")
     w32 = 0 if w_q is None else _need_norm_weights(w_q, w_k, D, dev)
     q_out = _out("q_out", q_out, q)
-    _run(dev, "s2attn_cache_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), None if w_q is None else
-         w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), table.data_ptr(), positions.data_ptr(),
-         slots.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, H, Hkv, D, rows, nb * bs, w32,
-         float(eps))
+    _run(dev, "s2attn_cache_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), _optional("w_q", w_q),
+         _optional("w_k", w_k), table.data_ptr(), positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(),
+         k_cache.data_ptr(), v_cache.data_ptr(), T, H, Hkv, D, rows, nb * bs, w32, float(eps))
     return q_out
 
 
@@ -767,6 +778,6 @@ def cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mas
         _need("lse", lse, (H, T), torch.float32, device=dev)
     workspace, wsb = _workspace("s2attn_cache_attn", workspace, _lib.s2attn_cache_attn_workspace_bytes(D), dev)
     _run(dev, "s2attn_cache_attn", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-         ctx_lens.data_ptr(), cu_seqlens.data_ptr(), None if mask is None else mask.data_ptr(), out.data_ptr(),
+         ctx_lens.data_ptr(), cu_seqlens.data_ptr(), _optional("mask", mask), out.data_ptr(),
          lse.data_ptr(), T, R, H, Hkv, D, nb, bs, maxb, workspace.data_ptr(), wsb)
     return out, lse

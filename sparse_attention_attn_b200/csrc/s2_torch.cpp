@@ -33,11 +33,12 @@ struct Calls {
 } calls;
 
 // The tensor of a plain torch.Tensor or Parameter, else null (subclasses take the Python path).  A tensor
-// inside torch.vmap or torch.func.grad is of the plain type too, but has no memory of its own: null.
+// inside torch.vmap, torch.func.grad or functionalize is of the plain type too, but has no memory of its
+// own: null (the address 0 of an optional operand would read as its absence).
 const at::Tensor* plain(PyObject* o) {
   if (!THPVariable_CheckExact(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  return t.has_storage() ? &t : nullptr;
+  return t.has_storage() && (t.numel() == 0 || t.const_data_ptr() != nullptr) ? &t : nullptr;
 }
 
 bool fits(const at::Tensor* t, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {

@@ -1,5 +1,5 @@
-"""Tensors inside torch's function transforms (vmap, grad, jvp) have the plain
-tensor type and no memory.  The compiled way into the norm and decoding calls
+"""Tensors inside torch's function transforms (vmap, grad, jvp, functionalize)
+have the plain tensor type and no memory.  The compiled way into the norm and decoding calls
 must leave them to the Python functions, which raise.
 
 On the CPU: a copy of csrc/s2_torch.cpp with its device conditions taken out
@@ -21,12 +21,16 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 # operand of each call that the transform takes (the plan has whole numbers alone: vmap only)
 CASES = [(n, i, how) for n, ops in (("qknorm_fwd", (0, 3)), ("qknorm_bwd", (0, 5)), ("cache_append", (0, 6)),
                                     ("cache_attention", (0, 2))) for i in ops for how in ("vmap", "grad", "jvp")]
+CASES += [("cache_attention", 6, "functionalize"), ("cache_append", 8, "functionalize"), ("cache_append", 9, "functionalize"),
+          ("cache_plan", 6, "functionalize"), ("qknorm_fwd", 2, "functionalize")]
 CASES += [("cache_plan", 0, "vmap"), ("cache_plan", 2, "vmap"), ("cache_attention", 4, "vmap")]
 
 
 def _transformed(call, x, how):
     if how == "vmap":
         return torch.vmap(call)(torch.stack([x, x]))
+    if how == "functionalize":  # its tensors have the address 0
+        return torch.func.functionalize(call)(x)
     if how == "grad":
         return torch.func.grad(call)(x)
     return torch.func.jvp(call, (x,), (torch.ones_like(x),))
@@ -76,6 +80,13 @@ def test_transformed_tensors_are_left_to_python(tmp_path):
     assert r.returncode == 0 and r.stdout.endswith("done\n"), (r.returncode, r.stdout[-300:], r.stderr[-2000:])
 
 
+def test_an_operand_without_memory_is_not_an_absent_one():
+    x = torch.zeros(3)
+    assert api._optional("mask", None) is None and api._optional("mask", x) == x.data_ptr()
+    with pytest.raises(ValueError, match="mask has no memory"):
+        torch.func.functionalize(lambda t: api._optional("mask", t))(x)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("compiled", [True, False])
 @pytest.mark.parametrize("name", NAMES)
@@ -88,7 +99,7 @@ def test_public_calls_raise_under_transforms(monkeypatch, name, compiled):
         if n != name:
             continue
         a = _args("cuda")[n]
-        with pytest.raises(RuntimeError, match="storage|data pointer"):
+        with pytest.raises((RuntimeError, ValueError), match="storage|data pointer|INVALID_ARG|no memory"):
             _transformed(lambda x: _public(n, [*a[:i], x, *a[i + 1:]])[0].float().sum(), a[i], how)
     want = _public(name, _args("cuda")[name])  # and the next usual call is as ever
     torch.cuda.synchronize()
