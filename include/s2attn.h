@@ -366,11 +366,15 @@ S2ATTN_API int s2attn_qknorm_rope_bwd(const void* q, const void* k, const void* 
  *   slots      [T]      the token's slot, -1 where no block is left for it
  *                       (free list or table row used up; the table's entry is
  *                       then -1 too, if it has one);
- *   counts     [4]      blocks taken, blocks needed, total of new_lens, tokens
- *                       left without a slot for want of a block.
+ *   counts     [4]      blocks taken (the first counts[0] of free_blocks are in
+ *                       the tables now, the others are still free), blocks that
+ *                       all new tokens need, total of new_lens, new tokens for
+ *                       which the free list or the table's row has no block.
+ * An entry below 0 among the ceil(ctx/block_size) that a row should have gives
+ * its tokens slot -1; counts[3] does not count them.
  * T is the length of positions and slots: entries behind the total get
  * position 0, slot -1 and mask 0, tokens behind T are dropped (counts[2] > T),
- * with the blocks only they would open.  parents (int32 [T], or NULL): the
+ * and the blocks only they would open are not taken.  parents (int32 [T], or NULL): the
  * tokens of a request are a tree of drafts, parents[t] the index in the
  * request of the draft before it, earlier than itself, or -1 (anything else
  * counts as -1); mask (int64 [T], NULL exactly when parents is) then gets bit j

@@ -12,7 +12,7 @@ def plan(ctx_lens, new_lens, block_tables, free_blocks, block_size, num_tokens, 
     cu = [0]
     pos, slots = np.zeros(T, np.int64), np.full(T, -1, np.int64)
     mask = np.zeros(T, np.uint64)
-    wanted = lost = 0
+    wanted = taken = lost = 0
     for i, (ctx, new) in enumerate(zip(ctx_lens, new_lens)):
         ctx, new = max(int(ctx), 0), max(int(new), 0)
         have = min(-(-ctx // bs), width)
@@ -31,6 +31,7 @@ def plan(ctx_lens, new_lens, block_tables, free_blocks, block_size, num_tokens, 
                 continue
             if b in opened and p % bs == 0:
                 tab[i, b] = blk
+                taken += blk >= 0  # a block is taken when a table names it
             if blk >= 0:
                 slots[t] = blk * bs + p % bs
             depth, bits = j, 0
@@ -46,7 +47,7 @@ def plan(ctx_lens, new_lens, block_tables, free_blocks, block_size, num_tokens, 
             mask[t] = np.uint64(bits)
             pos[t] = ctx + depth
         cu.append(cu[-1] + new)
-    counts = [min(wanted, len(free_blocks)), wanted, cu[-1], lost]
+    counts = [taken, wanted, cu[-1], lost]
     return np.array(cu), pos, slots, mask.view(np.int64), np.array(counts), tab
 
 

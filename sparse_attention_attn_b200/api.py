@@ -654,7 +654,7 @@ class CachePlan(NamedTuple):
     positions: torch.Tensor           # [T] position for the rotation
     slots: torch.Tensor               # [T] slot in the cache, -1: none
     mask: Optional[torch.Tensor]      # [T] visible drafts of a tree, None without parents
-    counts: torch.Tensor              # [4] blocks taken, needed, new tokens, tokens left without a block
+    counts: torch.Tensor              # [4] free blocks taken (the first ones), needed, new tokens, those without a block
 
 
 def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, num_tokens: int, parents=None):
