@@ -286,6 +286,19 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       if (sg.tiles < 0) break;
       const uint32_t sq = sbase + C::OFF_Q + qs * C::QSLOT;
       const int rows = sg.ntok * a.rep;
+      // what the lane's row (h: the first or the second) sees: up to its last key (chains), or the draft bits
+      struct Sight {
+        int last;
+        unsigned long long drafts;
+      };
+      auto sight_of = [&](int h) {
+        const int row = (lane >> 2) + 8 * h, j = sg.tok + (row < rows ? row / a.rep : 0);
+        return Sight{min(sg.ctx + j, sg.keys - 1), a.mask != nullptr ? visible_drafts(a, sg, sg.row0 + j) : 0ull};
+      };
+      auto sees = [&](const Sight& s, int key) {
+        const int d = key - sg.ctx;
+        return a.mask == nullptr ? key <= s.last : d < 0 || (d < 64 && (s.drafts >> (d & 63) & 1));
+      };
       float o[D / 8][4];
 #pragma unroll
       for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
@@ -331,17 +344,13 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           if (key0 + 16 > sg.ctx) {  // some key of the warp is a draft or behind the last
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              // what the lane's row sees: up to its last key (chains), or the draft bits
-              const int row = (lane >> 2) + 8 * h, j = sg.tok + (row < rows ? row / a.rep : 0);
-              const int last_key = min(sg.ctx + j, sg.keys - 1);
-              const unsigned long long see = a.mask != nullptr ? visible_drafts(a, sg, sg.row0 + j) : 0ull;
+              const Sight sight = sight_of(h);
 #pragma unroll
               for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int key = key0 + n * 8 + (lane & 3) * 2 + e, d = key - sg.ctx;
-                  const bool vis = a.mask == nullptr ? key <= last_key : d < 0 || (d < 64 && (see >> (d & 63) & 1));
-                  if (!vis) sc[n][2 * h + e] = neg_inf();
+                  const int key = key0 + n * 8 + (lane & 3) * 2 + e;
+                  if (!sees(sight, key)) sc[n][2 * h + e] = neg_inf();
                 }
             }
           }
@@ -394,10 +403,12 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           if (odd) {
             for (int key = 0; key < 16 && key0 + key < sg.keys; ++key) {
               float p[2];
+              bool seen[2];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t w = __shfl_sync(0xffffffffu, key < 8 ? pf[h] : pf[h + 2], (lane & ~3) | ((key & 7) >> 1));
                 p[h] = __uint_as_float(key & 1 ? w & 0xffff0000u : w << 16);
+                seen[h] = sees(sight_of(h), key0 + key);
               }
 #pragma unroll
               for (int d = 0; d < D / 8; ++d) {
@@ -405,9 +416,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(swz(sv, C::SLAB, warp * 16 + key, d) + (lane & 3) * 4));
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  if (p[h] == 0.f) continue;  // not seen
-                  o[d][2 * h] = fmaf(p[h], __uint_as_float(w << 16), o[d][2 * h]);
-                  o[d][2 * h + 1] = fmaf(p[h], __uint_as_float(w & 0xffff0000u), o[d][2 * h + 1]);
+                  if (!seen[h]) continue;
+                  const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
+                  // (a weight that underflowed is not 0: such a value is still itself)
+                  o[d][2 * h] = p[h] == 0.f && !isfinite(v0) ? o[d][2 * h] + v0 : fmaf(p[h], v0, o[d][2 * h]);
+                  o[d][2 * h + 1] = p[h] == 0.f && !isfinite(v1) ? o[d][2 * h + 1] + v1 : fmaf(p[h], v1, o[d][2 * h + 1]);
                 }
               }
             }
