@@ -476,8 +476,8 @@ S2ATTN_API int s2attn_selftest_wait_timeout(uint32_t* status_out, uint64_t limit
 
 /*
  * 1 if this library is the debug build (libs2attn_debug.so, compiled with
- * S2ATTN_DEBUG_CHECKS): its kernels check every computed global index
- * against its tensor before the access, skip an access that falls outside
+ * S2ATTN_DEBUG_CHECKS): its kernels check the global indexes that they compute
+ * against their tensors before the access, skip an access that falls outside
  * and record S2ATTN_ERR_DEVICE_BOUNDS with the site in the device status word
  * (read by s2attn_device_status).  0 for the default build, which has no
  * such checks.

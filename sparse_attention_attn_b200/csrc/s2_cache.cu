@@ -152,7 +152,9 @@ __global__ void __launch_bounds__(kPlanThreads) s2_cache_plan_kernel(CachePlanAr
   int blk = -1;
   if (col < static_cast<uint32_t>(a.max_blocks)) {
     int* entry = a.block_tables + static_cast<size_t>(i) * a.max_blocks + col;
-    if (col < have) {
+    if (!in_bounds(a.status, i, a.R, 730)) {
+      blk = -1;
+    } else if (col < have) {
       blk = *entry;
     } else {
       const uint32_t f = static_cast<uint32_t>(first[m]) + (col - have);
@@ -169,6 +171,9 @@ __global__ void __launch_bounds__(kPlanThreads) s2_cache_plan_kernel(CachePlanAr
     int at = j;
     for (;;) {
       const long long x = static_cast<long long>(cu[m]) + at - (t0 - kPlanBack);
+      if (!in_bounds(a.status, x >= 0 ? x : 0, kPlanBack + kPlanThreads, 731) ||
+          !in_bounds(a.status, static_cast<long long>(cu[m]) + at, a.T, 732))
+        break;
       const int up = x >= 0 ? par[x] : a.parents[static_cast<long long>(cu[m]) + at];
       if (up < 0 || up >= at) break;  // a parent comes before its child
       if (up < 64) bits |= 1ull << up;

@@ -57,6 +57,18 @@ __device__ __forceinline__ int visible_keys(const CacheAttnArgs& a, const Req& r
   return a.mask != nullptr ? r.keys : min(r.ctx + min(tokens, r.keys - r.ctx), r.keys);
 }
 
+// Debug build: row (token tk, query head) lies in o and lse.
+__device__ __forceinline__ bool row_in(const CacheAttnArgs& a, int tk, int head, uint32_t where) {
+  return in_bounds(a.status, tk, a.T, where) && in_bounds(a.status, head, a.H, where);
+}
+
+// The block of request i's key, -1 where the debug build finds the entry outside the table.
+__device__ __forceinline__ int block_of(const CacheAttnArgs& a, int i, int key) {
+  const int col = key >> a.bs_log2;
+  if (!in_bounds(a.status, i, a.R, 740) || !in_bounds(a.status, col, a.max_blocks, 741)) return -1;
+  return a.block_tables[static_cast<size_t>(i) * a.max_blocks + col];
+}
+
 struct Seg {
   int ri, kvh;
   int row0, ctx, keys;  // the request (row0: first row of q)
@@ -223,7 +235,7 @@ __device__ __noinline__ void add_odd(const CacheAttnArgs& a, const Seg& sg, int 
   const int j_tok = token - sg.row0, last = min((sg.kt0 + sg.tiles) * kTile, sg.keys);
   const unsigned long long see = a.mask != nullptr ? visible_drafts(a, sg, token) : 0ull;
   for (int key = max(sg.kt0 * kTile, sg.ctx); key < last; ++key) {
-    const int d = key - sg.ctx, blk = a.block_tables[static_cast<size_t>(sg.ri) * a.max_blocks + (key >> a.bs_log2)];
+    const int d = key - sg.ctx, blk = block_of(a, sg.ri, key);
     if (a.mask != nullptr ? d >= 64 || !(see >> d & 1) : d > j_tok) continue;
     if (blk < 0 || blk >= a.num_blocks) continue;
     const size_t place = (static_cast<size_t>(blk) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1));
@@ -306,7 +318,8 @@ template <int ROWS, int D>
 struct Part {
   static constexpr size_t kFloats = static_cast<size_t>(ROWS) * (D + 2);
   static __device__ __forceinline__ float* at(const CacheAttnArgs& a, int cta, int slot) {
-    return a.partial + (2 * static_cast<size_t>(cta) + slot) * kFloats;
+    const size_t off = (2 * static_cast<size_t>(cta) + slot) * kFloats;
+    return a.partial + (in_bounds(a.status, off + kFloats - 1, kCachePartFloats<D>, 742) ? off : 0);
   }
 };
 
@@ -418,6 +431,7 @@ __global__ void __launch_bounds__(256) s2_cache_join_kernel(CacheAttnArgs a) {
     const int tile = (row0 + i) / TILE, in = row0 + i - tile * TILE, jt = in / a.rep, tok = tile * a.tpt + jt;
     if (jt >= a.tpt || tok >= d.y) continue;  // a row of no token
     const int tk = d.x + tok, head = d.z * a.rep + in - jt * a.rep;
+    if (!row_in(a, tk, head, 743)) continue;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (static_cast<size_t>(tk) * a.H + head) * D + lane * PER);
 #pragma unroll

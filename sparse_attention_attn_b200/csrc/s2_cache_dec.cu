@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           mbar_arrive_expect_tx(smem_u32(&bar_qfull[qs]), a.tpt * a.rep * 128 * (D / 64));
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(sbase + C::OFF_Q + qs * C::QSLOT + c * C::QSLAB, &tmQ, smem_u32(&bar_qfull[qs]), c * 64,
-                        sg.kvh * a.rep, sg.row0 + sg.tok, 0);
+                        sg.kvh * a.rep, in_bounds(a.status, sg.row0 + sg.tok, a.T, 744) ? sg.row0 + sg.tok : 0, 0);
         } else {
           mbar_arrive(smem_u32(&bar_qfull[qs]));
         }
@@ -237,13 +237,12 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       __syncwarp();
       ++qu;
       if (!more) break;
-      const int* table = a.block_tables + static_cast<size_t>(sg.ri) * a.max_blocks;
       for (int i = 0; ok && i < sg.tiles; ++i) {
         const int key = (sg.kt0 + i) * kKeys + (lane << page_log2);
         const bool mine = lane < (kKeys >> page_log2) && key < sg.keys;
         int row = 0;  // a block outside the cache reads as zeros: its row lies behind the tensor
         if (mine) {
-          const int blk = table[key >> a.bs_log2];
+          const int blk = block_of(a, sg.ri, key);
           row = data_in_range(a.status, blk, a.num_blocks, 711) ? (blk << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))
                                                                 : a.num_blocks << a.bs_log2;
         }
@@ -502,6 +501,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         } else if (sg.whole) {
           const int jt = row / a.rep, head = sg.kvh * a.rep + row - jt * a.rep, tk = sg.row0 + sg.tok + jt;
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          if (!row_in(a, tk, head, 745)) continue;
           *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(tk) * a.H + head) * D + 4 * c) =
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
           if (c == 0) a.lse[static_cast<size_t>(head) * a.T + tk] = lse_of(mm, ll);
@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_empty[(L + NS - 1) % NS]));
       }
-      if (!CL && tid == 0 && sg.first && !sg.whole)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
+      if (!CL && tid == 0 && sg.first && !sg.whole && in_bounds(a.status, sg.last_cta, gridDim.x, 747))
+        // join work: the parts lie in CTAs blockIdx.x .. last_cta
         a.desc[blockIdx.x] = join_work(sg);
     }
   }
@@ -549,6 +550,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         }
         const int jt = row / a.rep, head = only.kvh * a.rep + row - jt * a.rep, tk = only.row0 + only.tok + jt;
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        if (!row_in(a, tk, head, 746)) continue;
         *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(tk) * a.H + head) * D + 4 * c) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         if (c == 0) a.lse[static_cast<size_t>(head) * a.T + tk] = lse_of(mm, ll);

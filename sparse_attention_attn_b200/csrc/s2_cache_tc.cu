@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         mbar_arrive_expect_tx(smem_u32(&bar_qfull[s]), a.tpt * a.rep * 128 * (D / 64));
         for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(q_addr(s) + c * C::ATOM, &tmQ, smem_u32(&bar_qfull[s]), c * 64, sg.kvh * a.rep, token, 0);
+          tma_load_4d(q_addr(s) + c * C::ATOM, &tmQ, smem_u32(&bar_qfull[s]), c * 64, sg.kvh * a.rep,
+                      in_bounds(a.status, token, a.T, 748) ? token : 0, 0);
       }
       __syncwarp();
       ++qu;
@@ -182,13 +183,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!more) break;
       if (sg.tiles == 0) continue;
       ok = load_q(sg.row0 + sg.tok) && (sg.ntok <= a.tpt || load_q(sg.row0 + sg.tok + a.tpt));
-      const int* table = a.block_tables + static_cast<size_t>(sg.ri) * a.max_blocks;
       for (int i = 0; ok && i < sg.tiles; ++i) {
         const int key = (sg.kt0 + i) * kTile + (lane << page_log2);
         const bool mine = lane < (kTile >> page_log2) && key < sg.keys;
         int row = 0;
         if (mine) {
-          const int blk = table[key >> a.bs_log2];
+          const int blk = block_of(a, sg.ri, key);
           row = data_in_range(a.status, blk, a.num_blocks, 711) ? (blk << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))
                                                                 : a.num_blocks << a.bs_log2;
         }
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool second = wg == 1 && !alt;  // this warpgroup worked on tile B
       const int jt = erow / a.rep, gtok = sg.row0 + sg.tok + (second ? a.tpt : 0) + jt;
       const int head = sg.kvh * a.rep + erow - jt * a.rep;
-      const bool live = jt < (second ? sg.ntok - a.tpt : min(sg.ntok, a.tpt));
+      const bool live = jt < (second ? sg.ntok - a.tpt : min(sg.ntok, a.tpt)) && row_in(a, gtok, head, 749);
       // where the row goes: o and lse, or this CTA's part (0: the item began before, 1: it begins here)
       float* part = Part<kPair, D>::at(a, blockIdx.x, sg.first);
       const int prow = (second ? kTile : 0) + row;
@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         finish(m_run, l_run);
       }
-      if (sg.first && !sg.whole && wg == 0 && row == 0)  // join work: the parts lie in CTAs blockIdx.x .. last_cta
+      if (sg.first && !sg.whole && wg == 0 && row == 0 && in_bounds(a.status, sg.last_cta, gridDim.x, 750))
+        // join work: the parts lie in CTAs blockIdx.x .. last_cta
         a.desc[blockIdx.x] = join_work(sg);
       put_seg(ng);
     }

@@ -460,6 +460,7 @@ struct QkNormArgs {
   void *dwq, *dwk;                 // backward: weight gradients [D]
   int tokens, N, H, Hkv;           // tokens = B N
   float eps;
+  uint32_t* status;                // debug build: where an index check records
 };
 constexpr int kQkNormMaxBlocks = 1024;  // blocks whose partial weight gradients the workspace holds
 
@@ -485,6 +486,7 @@ struct CachePlanArgs {
   int *cu_seqlens, *positions, *slots, *counts;  // [R+1], [T], [T], [4]
   unsigned long long* mask;        // [T] or null
   int R, max_blocks, num_free, block_size, T;
+  uint32_t* status;                // debug build: where an index check records
 };
 
 // Attention of new tokens over a paged cache.
@@ -506,6 +508,8 @@ struct CacheAttnArgs {
 constexpr int kCacheRows = 16;     // query rows of a tile of the few-row kernel
 constexpr int kCacheMinUnits = 2;  // key tiles a CTA of it takes at least
 constexpr int kCacheSms = 148;     // SMs the workspace is sized for (one CTA each, two of the few-row kernel)
+template <int D>
+constexpr long long kCachePartFloats = 4LL * kCacheSms * kTile * (D + 2);  // parts: two of 256 rows per SM
 
 cudaError_t launch_qknorm_fwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);
 cudaError_t launch_qknorm_bwd(const QkNormArgs& a, int D, int w_fp32, int num_sms, cudaStream_t stream);

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256) s2_qknorm_fwd_kernel(QkNormArgs a) {
   const long long n = static_cast<long long>(a.tokens) * G * CH;
   for (long long e0 = blockIdx.x * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += gridDim.x * 256LL) {
     const long long e = e0 + (threadIdx.x & 31u);
-    const bool live = e < n;
+    bool live = e < n;
     const int ch = static_cast<int>(e % CH);
     const uint32_t unit = live ? static_cast<uint32_t>(e / CH) : 0u;  // < 2^31 (checked by the host)
     const int tok = unit / G, gi = unit - tok * G;
@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(256) s2_qknorm_fwd_kernel(QkNormArgs a) {
     const int h0 = (is_q ? gi : gi - gq) * HG, heads = is_q ? a.H : a.Hkv;
     const __nv_bfloat16* src = (is_q ? a.q : a.k) + (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
     __nv_bfloat16* dst = (is_q ? a.yq : a.yk) + (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
+    live = live && in_bounds(a.status, tok, a.tokens, 720) && in_bounds(a.status, h0, heads, 721);
     uint4 u1[HG], u2[HG];
 #pragma unroll
     for (int k = 0; k < HG; ++k) {
@@ -217,9 +218,10 @@ __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
   const long long n = static_cast<long long>(a.tokens) * G * CH;
   for (long long e0 = block * 256LL + (threadIdx.x & ~31u); e0 < n; e0 += grid * 256LL) {
     const long long e = e0 + lane;
-    const bool live = e < n;
+    bool live = e < n;
     const uint32_t unit = live ? static_cast<uint32_t>(e / CH) : 0u;
     const int tok = unit / G, h0 = (unit - tok * G) * HG;
+    live = live && in_bounds(a.status, tok, a.tokens, 722) && in_bounds(a.status, h0, heads, 723);
     const size_t off = (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
     uint4 u1[HG], u2[HG], d1[HG], d2[HG];
 #pragma unroll
@@ -287,7 +289,8 @@ __global__ void __launch_bounds__(256, 2) s2_qknorm_bwd_kernel(QkNormArgs a) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
-    a.partial[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = t;
+    if (in_bounds(a.status, blockIdx.x, kQkNormMaxBlocks, 724))
+      a.partial[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = t;
   }
 }
 
@@ -303,6 +306,7 @@ __global__ void __launch_bounds__(1024) s2_qknorm_dw_kernel(QkNormArgs a) {
   const bool which = blockIdx.x >= D / 32;
   const int col = blockIdx.x % (D / 32) * 32 + lane;
   wait_for_primary();
+  if (!in_bounds(a.status, a.blocks - 1, kQkNormMaxBlocks, 725)) return;
   double t = 0.0;
   for (int b = (which ? a.blocks_q : 0) + warp; b < (which ? a.blocks : a.blocks_q); b += 32)
     t += a.partial[static_cast<size_t>(b) * D + col];
@@ -336,6 +340,7 @@ __global__ void __launch_bounds__(256) s2_cache_append_kernel(CacheAppendArgs a)
            data_in_range(a.status, pos, a.table_rows, 702);
     const int kind = gi < gq ? 0 : (gi < gq + gk ? 1 : 2);  // q, k, v
     const int h0 = (kind == 0 ? gi : (kind == 1 ? gi - gq : gi - gq - gk)) * HG, heads = kind == 0 ? a.H : a.Hkv;
+    live = live && in_bounds(a.status, tok, a.T, 726) && in_bounds(a.status, h0, heads, 727);
     const size_t from = (static_cast<size_t>(tok) * heads + h0) * D + ch * 8;
     const size_t to = kind == 0 ? from : (static_cast<size_t>(live ? slot : 0) * heads + h0) * D + ch * 8;
     const __nv_bfloat16* src = (kind == 0 ? a.q : (kind == 1 ? a.k : a.v)) + from;

@@ -905,6 +905,16 @@ bool status_block(uint32_t** out) {
   return e == cudaSuccess;
 }
 
+// The status block for kernels that record in it in the debug build alone (else null, and not asked for).
+bool debug_status_block(uint32_t** out) {
+#ifdef S2ATTN_DEBUG_CHECKS
+  return status_block(out);
+#else
+  *out = nullptr;
+  return true;
+#endif
+}
+
 // Shapes of the query/key norm: any number of tokens and heads.
 int validate_qknorm(int B, int N, int H, int Hkv, int D, double eps) {
   if (B <= 0 || N <= 0 || H <= 0 || Hkv <= 0 || D <= 0) return S2ATTN_ERR_INVALID_ARG;
@@ -1086,6 +1096,7 @@ int s2attn_qknorm_rope_fwd(const void* q, const void* k, const void* w_q, const 
   if (!device_info(&info)) return S2ATTN_ERR_CUDA;
   if (!info.ok) return S2ATTN_ERR_UNSUPPORTED;
   QkNormArgs a = qknorm_args(q, k, w_q, w_k, table, q_out, k_out, B, N, H, Hkv, eps);
+  if (!debug_status_block(&a.status)) return S2ATTN_ERR_CUDA;
   return launched(launch_qknorm_fwd(a, D, w_fp32 ? 1 : 0, info.sms, static_cast<cudaStream_t>(stream)), 1);
 }
 
@@ -1117,6 +1128,7 @@ int s2attn_qknorm_rope_bwd(const void* q, const void* k, const void* w_q, const 
   a.partial = static_cast<float*>(workspace);
   a.dwq = dw_q;
   a.dwk = dw_k;
+  if (!debug_status_block(&a.status)) return S2ATTN_ERR_CUDA;
   return launched(launch_qknorm_bwd(a, D, w_fp32 ? 1 : 0, info.sms, static_cast<cudaStream_t>(stream)), 2);
 }
 
@@ -1192,13 +1204,14 @@ int s2attn_cache_plan(const int* ctx_lens, const int* new_lens, int* block_table
   a.num_free = num_free;
   a.block_size = block_size;
   a.T = T;
+  if (!debug_status_block(&a.status)) return S2ATTN_ERR_CUDA;
   return launched(launch_cache_plan(a, info.sms, static_cast<cudaStream_t>(stream)), 1);
 }
 
 size_t s2attn_cache_attn_workspace_bytes(int D) {
   if (D != 64 && D != 128) return 0;
   // a descriptor per CTA (two an SM at most) and two parts of 256 rows per SM
-  return kCacheSms * (2 * sizeof(int4) + static_cast<size_t>(4) * kTile * (D + 2) * sizeof(float));
+  return kCacheSms * 2 * sizeof(int4) + (D == 64 ? kCachePartFloats<64> : kCachePartFloats<128>) * sizeof(float);
 }
 
 int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, const int* block_tables,
