@@ -33,12 +33,11 @@ struct Calls {
 } calls;
 
 // The tensor of a plain torch.Tensor or Parameter, else null (subclasses take the Python path).  A tensor
-// inside torch.vmap, torch.func.grad or functionalize is of the plain type too, but has no memory of its
-// own: null (the address 0 of an optional operand would read as its absence).
+// inside torch.vmap or torch.func.grad is of the plain type too, but has no memory of its own: null.
 const at::Tensor* plain(PyObject* o) {
   if (!THPVariable_CheckExact(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  return t.has_storage() && (t.numel() == 0 || t.const_data_ptr() != nullptr) ? &t : nullptr;
+  return t.has_storage() ? &t : nullptr;
 }
 
 bool fits(const at::Tensor* t, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {
@@ -120,6 +119,10 @@ at::Tensor piece(const at::Tensor& t, int64_t from, int64_t n) {
   return p;
 }
 
+// Whether the operand, where there is one, has memory: the address 0 (of a tensor inside functionalize)
+// would read as the operand's absence.
+bool there(const at::Tensor* t) { return t == nullptr || t->const_data_ptr() != nullptr; }
+
 PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
   PyObject* out = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
   if (out == nullptr) return nullptr;
@@ -196,17 +199,17 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const c10::Device dev = q->device();
   const int64_t T = q->size(0), H = q->size(1), D = q->size(2), Hkv = k->size(1), rows = table->size(0);
   const int64_t nb = kc->size(0), bs = kc->size(1);
-  const int w32 = norm ? weights(plain(args[8]), plain(args[9]), D, dev) : 0;
+  const at::Tensor *tq = norm ? plain(args[8]) : nullptr, *tk = norm ? plain(args[9]) : nullptr;
+  const int w32 = norm ? weights(tq, tk, D, dev) : 0;
   if (!small(Hkv) || !small(rows) || !small(nb) || !small(bs) || w32 < 0 || !fits(q, at::kBFloat16, {T, H, D}, dev) ||
       !fits(k, at::kBFloat16, {T, Hkv, D}, dev) || !fits(v, at::kBFloat16, {T, Hkv, D}, dev) ||
       !fits(table, at::kFloat, {rows, D / 2, 2}, dev) || !fits(pos, at::kInt, {T}, dev) ||
       !fits(slots, at::kInt, {T}, dev) || !fits(kc, at::kBFloat16, {nb, bs, Hkv, D}, dev) ||
       !fits(vc, at::kBFloat16, {nb, bs, Hkv, D}, dev) ||
-      (!fresh && !fits(plain(args[11]), at::kBFloat16, {T, H, D}, dev)))
+      (!fresh && !fits(plain(args[11]), at::kBFloat16, {T, H, D}, dev)) || !there(tq) || !there(tk))
     Py_RETURN_NONE;
   at::Tensor out = fresh ? fresh_tensor(q->sizes(), at::kBFloat16, dev) : *plain(args[11]);
-  const void* wq = norm ? ptr(plain(args[8])) : nullptr;
-  const void* wk = norm ? ptr(plain(args[9])) : nullptr;
+  const void *wq = ptr(tq), *wk = ptr(tk);
   void* s = stream_of(*q);
   const int st = released([&] {
     return calls.append(ptr(*q), ptr(*k), ptr(*v), wq, wk, ptr<float>(*table), ptr<int>(*pos), ptr<int>(*slots), ptr(out),
@@ -237,7 +240,7 @@ PyObject* cache_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int64_t R = ctx->size(0), width = tab->size(1), nf = free_->size(0);
   if (!small(width) || !small(nf) || !fits(ctx, at::kInt, {R}, dev) || !fits(add, at::kInt, {R}, dev) ||
       !fits(tab, at::kInt, {R, width}, dev) || !fits(free_, at::kInt, {nf}, dev) ||
-      (tree && !fits(par, at::kInt, {T}, dev)))
+      (tree && !fits(par, at::kInt, {T}, dev)) || !there(par))
     Py_RETURN_NONE;
   at::Tensor buf = fresh_tensor({2 * T + R + 5}, at::kInt, dev), mask;  // one allocation for the int32 outputs
   if (tree) mask = fresh_tensor({T}, at::kLong, dev);
@@ -279,7 +282,7 @@ PyObject* cache_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
       !fits(q, at::kBFloat16, {T, H, D}, dev) || !fits(kc, at::kBFloat16, {nb, bs, Hkv, D}, dev) ||
       !fits(vc, at::kBFloat16, {nb, bs, Hkv, D}, dev) || !fits(tab, at::kInt, {R, width}, dev) ||
       !fits(plain(args[4]), at::kInt, {R}, dev) || !fits(plain(args[5]), at::kInt, {R + 1}, dev) ||
-      (masked && !fits(mask, at::kLong, {T}, dev)))
+      (masked && !fits(mask, at::kLong, {T}, dev)) || !there(mask))
     Py_RETURN_NONE;
   const size_t ws = calls.attn_ws(static_cast<int>(D));
   if (ws == 0) Py_RETURN_NONE;

@@ -22,7 +22,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CASES = [(n, i, how) for n, ops in (("qknorm_fwd", (0, 3)), ("qknorm_bwd", (0, 5)), ("cache_append", (0, 6)),
                                     ("cache_attention", (0, 2))) for i in ops for how in ("vmap", "grad", "jvp")]
 CASES += [("cache_attention", 6, "functionalize"), ("cache_append", 8, "functionalize"), ("cache_append", 9, "functionalize"),
-          ("cache_plan", 6, "functionalize"), ("qknorm_fwd", 2, "functionalize")]
+          ("cache_plan", 6, "functionalize")]  # (the C calls refuse the address 0 of the other operands)
 CASES += [("cache_plan", 0, "vmap"), ("cache_plan", 2, "vmap"), ("cache_attention", 4, "vmap")]
 
 
