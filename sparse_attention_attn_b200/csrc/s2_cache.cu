@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kPlanThreads) s2_cache_plan_kernel(CachePlanAr
     }
   __syncthreads();
   unsigned long long run = 0;  // tokens (high word) and new blocks (low word) before this chunk
-  unsigned long long tally = 0;  // of block 0: tokens without a block (high word), blocks opened by tokens before T (low)
+  unsigned long long lost = 0;
   for (int base = 0; base < a.R; base += kPlanThreads * kPlanPer) {
     unsigned long long v[kPlanPer], sum = 0;
     int ctx[kPlanPer], n[kPlanPer];
@@ -87,14 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) s2_cache_plan_kernel(CachePlanAr
           const uint32_t got = min(static_cast<uint32_t>(v[k]), left);
           const long long last = static_cast<long long>(ctx[k]) + n[k];
           const long long end = max(static_cast<long long>(have + got) * bs, static_cast<long long>(ctx[k]));
-          if (last > end) tally += static_cast<unsigned long long>(last - end) << 32;
-          // blocks that a token before T opens (the others stay in the free list)
-          uint32_t opened = static_cast<uint32_t>(v[k]);
-          if (a.T - c < n[k]) {
-            const unsigned long long kept = static_cast<unsigned long long>(ctx[k]) + max(a.T - c, 0LL);
-            opened = min(static_cast<uint32_t>((kept + bs - 1) / bs), static_cast<uint32_t>(a.max_blocks)) - have;
-          }
-          tally += opened;
+          if (last > end) lost += last - end;
         }
         if (n[k] > 0 && c < t1 && c + n[k] > t0) {
           const int p = static_cast<int>((c > t0 ? c : t0) - t0);
@@ -108,21 +101,23 @@ __global__ void __launch_bounds__(kPlanThreads) s2_cache_plan_kernel(CachePlanAr
     }
     run = all;
     __syncthreads();  // wsum is reused; markers are complete after the last chunk
-    if (blockIdx.x != 0 && static_cast<long long>(run >> 32) >= t1) break;
+    if (blockIdx.x != 0 && static_cast<long long>(run >> 32) > t1) break;  // (the last block sees whether tokens are dropped)
   }
   if (blockIdx.x == 0) {
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) tally += __shfl_xor_sync(0xffffffffu, tally, m);
-    if (lane == 0) wsum[warp] = tally;
+    for (int m = 16; m > 0; m >>= 1) lost += __shfl_xor_sync(0xffffffffu, lost, m);
+    if (lane == 0) wsum[warp] = lost;
     __syncthreads();
     if (tid == 0) {
-      unsigned long long all = 0;
-      for (int w = 0; w < kPlanThreads / 32; ++w) all += wsum[w];
+      unsigned long long l = 0;
+      for (int w = 0; w < kPlanThreads / 32; ++w) l += wsum[w];
+      const uint32_t needed = static_cast<uint32_t>(run);
       a.cu_seqlens[a.R] = static_cast<int>(run >> 32);
-      a.counts[0] = static_cast<int>(min(static_cast<uint32_t>(all), static_cast<uint32_t>(a.num_free)));
-      a.counts[1] = static_cast<int>(static_cast<uint32_t>(run));
+      if (static_cast<long long>(run >> 32) <= a.T)  // (else the last token kept writes it)
+        a.counts[0] = static_cast<int>(min(needed, static_cast<uint32_t>(a.num_free)));
+      a.counts[1] = static_cast<int>(needed);
       a.counts[2] = static_cast<int>(run >> 32);
-      a.counts[3] = static_cast<int>(all >> 32);
+      a.counts[3] = static_cast<int>(l);
     }
   }
   // the request of every token of the window: the last marker at or before it
@@ -149,6 +144,11 @@ __global__ void __launch_bounds__(kPlanThreads) s2_cache_plan_kernel(CachePlanAr
   const uint32_t place = static_cast<uint32_t>(ctx) + static_cast<uint32_t>(j);
   const uint32_t col = place / bs, row = place - col * bs;
   const uint32_t have = min((static_cast<uint32_t>(ctx) + bs - 1) / bs, static_cast<uint32_t>(a.max_blocks));
+  // the last token kept, others behind it dropped: the blocks up to its own are taken
+  if (t == a.T - 1 && static_cast<long long>(run >> 32) > a.T) {
+    const uint32_t opened = first[m] + max(min(col + 1, static_cast<uint32_t>(a.max_blocks)), have) - have;
+    a.counts[0] = static_cast<int>(min(opened, static_cast<uint32_t>(a.num_free)));
+  }
   int blk = -1;
   if (col < static_cast<uint32_t>(a.max_blocks)) {
     int* entry = a.block_tables + static_cast<size_t>(i) * a.max_blocks + col;

@@ -905,12 +905,12 @@ bool status_block(uint32_t** out) {
   return e == cudaSuccess;
 }
 
-// The status block for kernels that record in it in the debug build alone (else null, and not asked for).
-bool debug_status_block(uint32_t** out) {
+// The status block for kernels that record in it in the debug build alone.
+bool debug_status_block(DebugStatus* d) {
 #ifdef S2ATTN_DEBUG_CHECKS
-  return status_block(out);
+  return status_block(&d->status);
 #else
-  *out = nullptr;
+  (void)d;
   return true;
 #endif
 }
@@ -1096,7 +1096,7 @@ int s2attn_qknorm_rope_fwd(const void* q, const void* k, const void* w_q, const 
   if (!device_info(&info)) return S2ATTN_ERR_CUDA;
   if (!info.ok) return S2ATTN_ERR_UNSUPPORTED;
   QkNormArgs a = qknorm_args(q, k, w_q, w_k, table, q_out, k_out, B, N, H, Hkv, eps);
-  if (!debug_status_block(&a.status)) return S2ATTN_ERR_CUDA;
+  if (!debug_status_block(&a)) return S2ATTN_ERR_CUDA;
   return launched(launch_qknorm_fwd(a, D, w_fp32 ? 1 : 0, info.sms, static_cast<cudaStream_t>(stream)), 1);
 }
 
@@ -1128,7 +1128,7 @@ int s2attn_qknorm_rope_bwd(const void* q, const void* k, const void* w_q, const 
   a.partial = static_cast<float*>(workspace);
   a.dwq = dw_q;
   a.dwk = dw_k;
-  if (!debug_status_block(&a.status)) return S2ATTN_ERR_CUDA;
+  if (!debug_status_block(&a)) return S2ATTN_ERR_CUDA;
   return launched(launch_qknorm_bwd(a, D, w_fp32 ? 1 : 0, info.sms, static_cast<cudaStream_t>(stream)), 2);
 }
 
@@ -1204,7 +1204,7 @@ int s2attn_cache_plan(const int* ctx_lens, const int* new_lens, int* block_table
   a.num_free = num_free;
   a.block_size = block_size;
   a.T = T;
-  if (!debug_status_block(&a.status)) return S2ATTN_ERR_CUDA;
+  if (!debug_status_block(&a)) return S2ATTN_ERR_CUDA;
   return launched(launch_cache_plan(a, info.sms, static_cast<cudaStream_t>(stream)), 1);
 }
 

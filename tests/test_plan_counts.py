@@ -13,6 +13,8 @@ CASES = [
     ([4, 8, 0], [4, 4, 9], 4, 3, 9, 4), ([4, 8, 0], [4, 4, 9], 4, 3, 9, 5), ([4, 8, 0], [4, 4, 9], 4, 3, 9, 13),
     ([4, 8, 0], [4, 4, 9], 4, 3, 1, 9), ([0] * 40, [7] * 40, 16, 2, 64, 100), ([15] * 300, [2] * 300, 16, 2, 250, 333),
     ([100, 3], [50, 50], 8, 13, 40, 60), ([0], [1000], 16, 70, 70, 1), ([0] * 1100, [1] * 1100, 1, 1, 2000, 1050),
+    ([0] * 1100, [1] * 1100, 1, 1, 2000, 1024), ([0] * 1100, [1] * 1100, 1, 1, 2000, 1100), ([0] * 300, [1] * 300, 1, 1, 9, 256),
+    ([5] * 1024 + [0] * 7, [1] * 1024 + [9] * 7, 4, 3, 3000, 1024), ([90] * 9, [40] * 9, 8, 12, 60, 100),
 ]
 
 
