@@ -151,6 +151,12 @@ __device__ __forceinline__ bool find_item(const CacheAttnArgs& a, int at, Req& r
   return false;
 }
 
+// Waits (bounded) for the last fill of every slot of a ring.  Out of line, away from what a small call has to
+// fetch (one token over 4097 keys: 12.6 us a call, 13.0 in line).
+__device__ __noinline__ void drain_ring(uint32_t bars, int slots, int fills) {
+  for (int s = 0; s < slots && s < fills; ++s) drain_wait(bars + 8 * s, ((fills - 1 - s) / slots) & 1);
+}
+
 // CL: the form for few items.  Each gets a cluster of CTAs (one or more) with an
 // equal share of its key tiles, which joins its parts through distributed shared
 // memory: one launch, no table of work and nothing in the workspace.
@@ -261,11 +267,12 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       }
       if (!ok) break;
     }
-    if (*wc.abort && lane == 0) {
-      // never leave copies in flight into shared memory: wait (bounded) for
-      // the last fill of every slot
-      for (int s = 0; s < NQ && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / NQ) & 1);
-      for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
+    if ((!CL || *wc.abort) && lane == 0) {
+      // never leave copies in flight into shared memory, whether or not a
+      // consumer has given up by now: it can do so after this warp's last copy
+      // (in clusters that is asked after the meeting, off the way of small calls)
+      drain_ring(smem_u32(bar_qfull), NQ, qu);
+      drain_ring(smem_u32(bar_full), NS, L);
     }
   } else {
     // ------------------------------------------------------------ consumers
@@ -285,19 +292,6 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       if (sg.tiles < 0) break;
       const uint32_t sq = sbase + C::OFF_Q + qs * C::QSLOT;
       const int rows = sg.ntok * a.rep;
-      // what the lane's row (h: the first or the second) sees: up to its last key (chains), or the draft bits
-      struct Sight {
-        int last;
-        unsigned long long drafts;
-      };
-      auto sight_of = [&](int h) {
-        const int row = (lane >> 2) + 8 * h, j = sg.tok + (row < rows ? row / a.rep : 0);
-        return Sight{min(sg.ctx + j, sg.keys - 1), a.mask != nullptr ? visible_drafts(a, sg, sg.row0 + j) : 0ull};
-      };
-      auto sees = [&](const Sight& s, int key) {
-        const int d = key - sg.ctx;
-        return a.mask == nullptr ? key <= s.last : d < 0 || (d < 64 && (s.drafts >> (d & 63) & 1));
-      };
       float o[D / 8][4];
 #pragma unroll
       for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
@@ -343,13 +337,17 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           if (key0 + 16 > sg.ctx) {  // some key of the warp is a draft or behind the last
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const Sight sight = sight_of(h);
+              // what the lane's row sees: up to its last key (chains), or the draft bits
+              const int row = (lane >> 2) + 8 * h, j = sg.tok + (row < rows ? row / a.rep : 0);
+              const int last_key = min(sg.ctx + j, sg.keys - 1);
+              const unsigned long long see = a.mask != nullptr ? visible_drafts(a, sg, sg.row0 + j) : 0ull;
 #pragma unroll
               for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int key = key0 + n * 8 + (lane & 3) * 2 + e;
-                  if (!sees(sight, key)) sc[n][2 * h + e] = neg_inf();
+                  const int key = key0 + n * 8 + (lane & 3) * 2 + e, d = key - sg.ctx;
+                  const bool vis = a.mask == nullptr ? key <= last_key : d < 0 || (d < 64 && (see >> (d & 63) & 1));
+                  if (!vis) sc[n][2 * h + e] = neg_inf();
                 }
             }
           }
@@ -407,7 +405,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               for (int h = 0; h < 2; ++h) {
                 const uint32_t w = __shfl_sync(0xffffffffu, key < 8 ? pf[h] : pf[h + 2], (lane & ~3) | ((key & 7) >> 1));
                 p[h] = __uint_as_float(key & 1 ? w & 0xffff0000u : w << 16);
-                seen[h] = sees(sight_of(h), key0 + key);
+                const int row = (lane >> 2) + 8 * h, j = sg.tok + (row < rows ? row / a.rep : 0), d = key0 + key - sg.ctx;
+                seen[h] = a.mask == nullptr ? d <= j : d < 0 || (d < 64 && (visible_drafts(a, sg, sg.row0 + j) >> d & 1));
               }
 #pragma unroll
               for (int d = 0; d < D / 8; ++d) {
@@ -528,6 +527,10 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     // of CTAs that have not ended, whatever it holds.
     static_assert(kRows * D * 4 <= 2 * C::QSLOT, "the part fits the free query slots");
     cluster_meet();
+    if (warp == kWarps && lane == 0 && *wc.abort) {
+      drain_ring(smem_u32(bar_qfull), NQ, 1);
+      drain_ring(smem_u32(bar_full), NS, only.tiles);
+    }
     const int rows = only.ntok * a.rep, parts = cluster_size();
     if (warp < kWarps)
       for (int e = cluster_rank() * (kWarps * 32) + tid; e < rows * (D / 4); e += parts * (kWarps * 32)) {

@@ -195,9 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = load_kv(&tmK, mine, row) && load_kv(&tmV, mine, row);
       }
     }
-    if (*wc.abort && lane == 0) {
+    if (lane == 0) {
       // never leave copies in flight into shared memory: wait (bounded) for
-      // the last fill of every slot
+      // the last fill of every slot -- always, since a consumer can give up
+      // after this warp has issued its last copy
       for (int s = 0; s < NQ && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / NQ) & 1);
       for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
     }
