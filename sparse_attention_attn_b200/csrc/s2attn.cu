@@ -947,21 +947,39 @@ bool cache_few_rows(int T, int R, int rep) {
 // than 8 clusters of 16, 32 of 8 or 256 CTAs in all are resident together.
 // Measured, us a call with clusters / without, 32 query and 8 kv heads of 128,
 // requests x keys: 1 x 1000 8.4 / 12.3 (16 CTAs an item), 1 x 4000 12.3 / 14.4,
-// 1 x 16000 22.5 / 24.7, 1 x 60000 55 / 54; 4 x 1000 10.3 / 12.9 (8), 4 x 2000
-// 12.3 / 14.5; 8 x 2000 18.9 / 22.7 (4), 8 x 200..4000 22.8 / 24.5; 16 x 2000
-// 28.8 / 34.6 (2), 16 x 200..4000 33.7 / 35.4; 32 x 1000 27.6 / 34.4 (1), 32 x
-// 200..4000 58 / 56; 64 x 500..1000 43 / 45 (1), 64 x 200..4000 105 / 97.  One
-// request, as many query as kv heads, 8 CTAs an item: 24 heads x 60000 keys
-// 115 / 122, 32 x 100000 239 / 256, 36 x 1000 14.4 / 12.3.
+// 1 x 4800 14.5 / 16.6, 1 x 16000 24.8 / 23.0; 4 x 1000 10.3 / 12.9 (8), 4 x 2400
+// 14.6 / 18.6, 4 x 8000 28.8 / 33.0; 8 x 1200 14.7 / 18.6 (4), 8 x 4000 28.9 /
+// 32.9, 8 x 200..4000 22.8 / 24.5; 16 x 600 14.6 / 18.6 (2), 16 x 2000 28.9 /
+// 33.0, 16 x 170..2000 24.8 / 22.9; 32 x 300 14.5 / 17.3 (1), 32 x 1000 27.7 /
+// 33.0; 64 x 300 24.3 / 24.7 (1), 64 x 1000 51 / 53, 64 x 80..1000 42 / 37; beyond
+// the limit 1 x 60000 55 / 54, 32 x 200..4000 58 / 56, 64 x 200..4000 105 / 97.
+// Heads of 64: 1 x 4800 10.5 / 14.5, 1 x 16000 19.2 / 18.6, 4 x 8000 20.6 / 23.1,
+// 32 x 1000 18.7 / 23.2, 64 x 50..1000 31 / 27.  One kv head: 1 x 4800 12.5 / 14.5, 1 x
+// 16000 22.7 / 18.6.
 // So: the largest cluster whose grid is resident (beyond, one CTA an item, up to
-// two waves), where a CTA's share is at most 1024 keys, or at any length where one
-// request nearly fills the grid.  Each CTA scans the requests on its own: few.
-int cache_cluster(int R, long long items, long long keys, int sms) {
+// two waves), where a CTA's share is at most 1024 keys: towards that limit equal
+// shares gain up to 5 us on equal lengths and lose up to 6 us on very unequal
+// ones, or where the clusters leave most SMs idle.  Each CTA scans the requests on
+// its own: few.
+// At any length, where one request fills the resident CTAs.  As many query as kv
+// heads, one token, 9000 / 30000 / 100000 keys; heads of 128, 8 CTAs an item: 24
+// heads 26 62 184 / 31 69 190, 32 32 81 247 / 37 86 262; 4: 48 43 116 363 / 47 123
+// 365, 64 54 149 469 / 59 157 495; 2: 96 79 226 751 / 80 233 708, 112 86 249 824 /
+// 93 260 838, 128 93 285 912 / 101 301 952; 1: 192 151 444 1495 / 143 433 1425, 224
+// 152 486 1658 / 166 517 1663, 256 172 547 1844 / 188 586 1915.  Heads of 64, where
+// a CTA's load is half as long: 32 heads (8) 21 46 132 / 25 51 134 and 64 (4) 33 82
+// 254 / 37 89 259, but 28 20 44 126 / 23 46 119, 48 31 80 241 / 31 69 198, 128 (2)
+// 60 178 492 / 61 163 522, 256 (1) 106 306 1077 / 101 304 1006.
+bool cache_one_fills(long long ctas, int c, int D) {
+  if (D == 64) return c >= 4 && ctas == 256;
+  return ctas >= (c >= 4 ? 192 : 224) && ctas <= 256;
+}
+int cache_cluster(int R, long long items, long long keys, int D, int sms) {
   const std::string v = override_value(tile_override(), "cache");
   const int c = items <= 8 ? 16 : items <= 32 ? 8 : items <= 64 ? 4 : items <= 128 ? 2 : 1;
   if (v == "cluster") return items < (1 << 20) ? c : 0;
   if (v == "dec" || sms < kCacheSms || R > 128 || items > 4 * kCacheSms) return 0;
-  return keys <= 1024 * c || (R == 1 && items * c >= 192 && items * c <= 256) ? c : 0;
+  return keys <= 1024 * c || (R == 1 && cache_one_fills(items * c, c, D)) ? c : 0;
 }
 
 QkNormArgs qknorm_args(const void* q, const void* k, const void* w_q, const void* w_k, const float* table, void* yq,
@@ -1277,7 +1295,7 @@ int s2attn_cache_attn(const void* q, const void* k_cache, const void* v_cache, c
   // row tiles the requests can have in all
   const int tiles = static_cast<int>((T + static_cast<long long>(std::min(R, T)) * (a.tpt - 1)) / a.tpt);
   const int cluster = cache_cluster(R, static_cast<long long>(Hkv) * tiles,
-                                    static_cast<long long>(max_blocks) * block_size, info.sms);
+                                    static_cast<long long>(max_blocks) * block_size, D, info.sms);
   if (cluster > 0) return launched(launch_cache_dec(tq, tk, tv, a, D, Hkv * tiles * cluster, cluster, s), 1);
   return launched(launch_cache_dec(tq, tk, tv, a, D, grid, 0, s), 2);
 }
