@@ -416,7 +416,18 @@ S2ATTN_API size_t s2attn_cache_attn_workspace_bytes(int D);
  * were.  Scale 1/sqrt(D); kv head of query head h is h / (H / Hkv).
  * Keys in a block outside [0, num_blocks) count as zero vectors (and are
  * recorded); places behind a row of block_tables do not exist.  Infinite and NaN
- * values of a new token's key or value reach only the rows that see it.
+ * values of a new token's key or value reach only the rows that see it, and
+ * make those infinite or NaN.
+ * Precision: scores, row maxima, sums and o are held in fp32; the softmax weights
+ * are rounded to bf16 for the product with V (their sums are taken before), as in
+ * s2attn_fwd, so o is off by up to 2^-8 of the weighted mean of |v| besides its own
+ * rounding to bf16.  Always so: there is no form that keeps fp32 weights.
+ * Which of two kernels runs, and in what form, follows from T, R, H / Hkv and the
+ * table's width alone (the lengths are not known here).  It changes the time and
+ * the last bits, so: leave requests without new tokens and rows of padding out
+ * where that is possible (4 requests with 64 drafts each among 252 idle ones take
+ * 392 us, alone 111), and take tables no wider than the step's longest request
+ * (one token over 4097 keys: 14.3 us, 16.1 with a table for more than 16384).
  * D in {64, 128}; H / Hkv <= 128; block_size a power of two from 16 to 256; T H <= 2^30;
  * num_blocks * block_size below 2^31, max_blocks * block_size at most 2^31 - 65536.
  * workspace: 16-byte aligned, s2attn_cache_attn_workspace_bytes(D) bytes, need
