@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(352, 1)
         __syncwarp();
       }
     }
-    if (*wc.abort && lane == 0) {
-      // never leave copies in flight into shared memory: wait (bounded) for
-      // the last fill of every stage and of the K/V buffer
+    if (lane == 0) {
+      // never leave copies in flight into shared memory (a role that gives up
+      // can do so after this warp's last copy): wait (bounded) for the last fill of every stage and of the K/V buffer
       if (kv_issued > 0) drain_wait(smem_u32(&bar_kv), (kv_issued - 1) & 1);
       for (int s = 0; s < ST && s < gi; ++s) drain_wait(smem_u32(&bar_full[s]), ((gi - 1 - s) / ST) & 1);
     }
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       }
     }
-    if (*wc.abort && lane == 0) {
+    if (lane == 0) {  // no copy is left in flight into shared memory, whichever role gives up, and when
       if (q_issued > 0) drain_wait(smem_u32(&bar_q), (q_issued - 1) & 1);
       for (int s = 0; s < ST && s < gi; ++s) drain_wait(smem_u32(&bar_kv[s]), ((gi - 1 - s) / ST) & 1);
     }

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(192, 1)
         __syncwarp();
       }
     }
-    if (*wc.abort && lane == 0) {
+    if (lane == 0) {  // no copy is left in flight into shared memory, whichever role gives up, and when
       for (int s = 0; s < ST && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / ST) & 1);
     }
   } else if (warp == 1) {

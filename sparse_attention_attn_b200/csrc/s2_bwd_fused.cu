@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(384, 1)
       ++nk;
       for (int it = pre; ok && it < iters; ++it) ok = load_stage(w, sh, it, nq);
     }
-    if (*wc.abort && lane == 0) {
-      // never leave copies in flight into shared memory: wait (bounded) for
-      // the last fill of K, V and every stage
+    if (lane == 0) {
+      // never leave copies in flight into shared memory (a role that gives up
+      // can do so after this warp's last copy): wait (bounded) for the last fill of K, V and every stage
       if (nk > 0) drain_wait(smem_u32(&bar_k), (nk - 1) & 1);
       if (nv > 0) drain_wait(smem_u32(&bar_v), (nv - 1) & 1);
       for (int s = 0; s < ST && s < gi; ++s) drain_wait(smem_u32(&bar_full[s]), ((gi - 1 - s) / ST) & 1);

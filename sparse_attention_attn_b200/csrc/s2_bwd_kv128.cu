@@ -182,8 +182,9 @@ __global__ void __launch_bounds__(352, 1)
         __syncwarp();
       }
     }
-    if (*wc.abort && lane == 0) {
-      // never leave copies in flight into shared memory
+    if (lane == 0) {
+      // never leave copies in flight into shared memory (a role that gives up
+      // can do so after this warp's last copy)
       if (kv_issued > 0) drain_wait(smem_u32(&bar_kv), (kv_issued - 1) & 1);
       for (int s = 0; s < ST && s < gi; ++s) drain_wait(smem_u32(&bar_full[s]), ((gi - 1 - s) / ST) & 1);
     }

@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(320, 1)
         it = itn;
       }
     }
-    if (*wc.abort && lane == 0) {
-      // never leave copies in flight into shared memory: wait (bounded) for
-      // the last fill of every slot
+    if (lane == 0) {
+      // never leave copies in flight into shared memory (a role that gives up
+      // can do so after this warp's last copy): wait (bounded) for the last fill of every slot
       for (int s = 0; s < NQ && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / NQ) & 1);
       for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
     }

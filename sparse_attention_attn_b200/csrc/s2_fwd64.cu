@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(320, 1)
         it = itn;
       }
     }
-    if (*wc.abort && lane == 0) {
+    if (lane == 0) {  // no copy is left in flight into shared memory, whichever role gives up, and when
       for (int s = 0; s < NQ && s < qu; ++s) drain_wait(smem_u32(&bar_qfull[s]), ((qu - 1 - s) / NQ) & 1);
       for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
     }

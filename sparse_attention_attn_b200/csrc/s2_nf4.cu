@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(Nf4Cfg<NS, DQW>::THREADS, 1)
         ++L;
       }
     }
-    if (*wc.abort && lane == 0) {
+    if (lane == 0) {  // no copy is left in flight into shared memory, whichever role gives up, and when
       for (int s = 0; s < NS && s < L; ++s) drain_wait(smem_u32(&bar_full[s]), ((L - 1 - s) / NS) & 1);
     }
   } else if (warp == 1) {
