@@ -661,8 +661,9 @@ def cache_plan(ctx_lens, new_lens, block_tables, free_blocks, block_size: int, n
     """Blocks, slots and positions for the new tokens of a ragged batch, on the
     GPU.  ctx_lens, new_lens int32 [R]: tokens in the cache and tokens to add;
     block_tables int32 [R, max_blocks]: the requests' blocks, extended in place
-    by blocks of free_blocks (int32, taken from its front in request order);
-    num_tokens: size of the token arrays, at least sum(new_lens).  parents
+    by blocks of free_blocks (int32, taken from its front in request order: drop
+    its first counts[0] entries before the next step); num_tokens: size of the
+    token arrays, at least sum(new_lens) (tokens behind it are dropped).  parents
     int32 [num_tokens]: the new tokens of each request are a tree of drafts,
     parents[t] the index in the request of the draft before it, -1 for the
     context.  Returns a CachePlan."""
@@ -752,7 +753,11 @@ def cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mas
     [R, max_blocks]).  Every row attends the earlier keys and, of the request's
     new ones, those its mask (int64 [T], bit j = new token j) names -- without
     mask those up to its own.  Returns (o [T, H, D] bf16, lse [H, T] fp32); rows
-    that see no key get 0 and -inf, rows of no request are left as they are."""
+    that see no key get 0 and -inf, rows of no request are left as they are.  The
+    softmax weights are rounded to bf16 for the product with V, all else is fp32.
+    The number of tokens, of requests and the tables' width choose the kernel:
+    tables no wider than the step's longest request, and no idle requests or
+    padding, are the fastest."""
     if out is None and lse is None and workspace is None:
         r = _fast.cache_attention(q, k_cache, v_cache, block_tables, ctx_lens, cu_seqlens, mask)
         if r is not None:

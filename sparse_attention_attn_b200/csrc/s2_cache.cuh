@@ -11,14 +11,13 @@
 // and cost nothing, so for a long prompt the runs are not alike: by the same
 // numbering, the busiest has 1.86 times the mean of a prompt of 4096 tokens (32/8
 // heads, no context; 494 us), 1.80 of 1024 (64/8), 1.29 of 4096 over 4096 (739 us).
-// `side` CTAs in a row work side by side:
-// each takes the same run of another kv head, so that what they read at a time
-// lies together in the cache (64 requests of 333 to 16384 keys, 8 kv heads: 342 us
-// with all 8 side by side, 349 one by one).  A segment is the part of an item
-// that lies in one CTA's run.  A segment that is not the whole item leaves
-// unnormalised sums, row maxima and row sums in the workspace, and the join
-// kernel adds the parts in order.  The split depends on the lengths and the SM
-// count alone, so the same call gives the same bits.
+// `side` CTAs in a row work side by side: each takes the same run of another kv
+// head, so that what they read at a time lies together in the cache (64 requests
+// of 333 to 16384 keys, 8 kv heads: 337 us so, 340 one head after the other).  A
+// segment is the part of an item that lies in one CTA's run.  A segment that is
+// not the whole item leaves unnormalised sums, row maxima and row sums in the
+// workspace, and the join kernel adds the parts in order.  The split depends on
+// the lengths and the SM count alone, so the same call gives the same bits.
 #pragma once
 
 #include <cuda.h>

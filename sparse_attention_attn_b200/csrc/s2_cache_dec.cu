@@ -25,8 +25,9 @@
 // memory.
 //
 // Measured, head dim 128 (bf16): 64 requests of 333 to 16384 keys, 32/8 heads,
-// 334 us, 6.65 TB/s, what a copy reaches; one request of 4097 keys, 32/8 heads,
-// 12.3 us (14.6 without clusters): latency.
+// 335 to 339 us, 6.6 TB/s, what a copy reaches; one request of 4097 keys, 32/8
+// heads, 12.6 us, 10.9 of it on the GPU (some 2 to 4 more without clusters):
+// latency.
 //
 // Rows of V behind the last key may hold anything (stale cache rows): the
 // fragments that hold them are zeroed in registers.
