@@ -35,23 +35,23 @@ class _Binding:
         if name not in self._NAMES:
             raise AttributeError(name)
         lib = _lib.load()
+        self.__dict__.update({n: lambda *args: None for n in self._NAMES})
         try:
             from . import _s2torch
-            ours = (lib.s2attn_header_hash().decode(), f"{torch.version.__version__} {torch.version.git_version}")
-            its = (getattr(_s2torch, "header_hash", None), getattr(_s2torch, "torch_version", None))
-            if its != ours:
-                warnings.warn(f"_s2torch.so was built for {its}, not for {ours}: its calls take the Python way until "
-                              "`python -m sparse_attention_attn_b200.build` is run", RuntimeWarning, stacklevel=3)
-                raise ImportError("_s2torch.so is of another build")
-            _s2torch.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
-                            ("s2attn_qknorm_rope_fwd", "s2attn_qknorm_rope_bwd",
-                             "s2attn_qknorm_rope_bwd_workspace_bytes", "s2attn_cache_append", "s2attn_cache_plan",
-                             "s2attn_cache_attn", "s2attn_cache_attn_workspace_bytes")))
-            calls = {n: getattr(_s2torch, n) for n in self._NAMES}
         except ImportError:
-            calls = {n: lambda *args: None for n in self._NAMES}
-        self.__dict__.update(calls)
-        return calls[name]
+            return self.__dict__[name]
+        ours = (lib.s2attn_header_hash().decode(), f"{torch.version.__version__} {torch.version.git_version}")
+        its = (getattr(_s2torch, "header_hash", None), getattr(_s2torch, "torch_version", None))
+        if its != ours:
+            warnings.warn(f"_s2torch.so was built for {its}, not for {ours}: its calls take the Python way until "
+                          "`python -m sparse_attention_attn_b200.build` is run", RuntimeWarning, stacklevel=3)
+            return self.__dict__[name]
+        _s2torch.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                        ("s2attn_qknorm_rope_fwd", "s2attn_qknorm_rope_bwd",
+                         "s2attn_qknorm_rope_bwd_workspace_bytes", "s2attn_cache_append", "s2attn_cache_plan",
+                         "s2attn_cache_attn", "s2attn_cache_attn_workspace_bytes")))
+        self.__dict__.update({n: getattr(_s2torch, n) for n in self._NAMES})
+        return self.__dict__[name]
 
 
 _fast = _Binding()

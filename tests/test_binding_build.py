@@ -4,6 +4,7 @@ import os
 import subprocess
 import sys
 import types
+import warnings
 
 import pytest
 import torch
@@ -39,6 +40,16 @@ def test_a_binding_of_another_build_is_not_called(monkeypatch, attrs):
     with pytest.warns(RuntimeWarning, match="_s2torch.so was built for"):
         assert b.cache_plan(1, 2, 3) is None
     assert all(getattr(b, n)() is None for n in NAMES) and seen == []
+
+
+def test_the_warning_as_an_error_comes_once(monkeypatch):
+    seen = _fake(monkeypatch)
+    b = api._Binding()
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(RuntimeWarning):
+            b.cache_plan
+        assert b.cache_plan(1) is None and b.qknorm_fwd() is None and seen == []
 
 
 def test_a_binding_of_this_build_is_bound(monkeypatch):
